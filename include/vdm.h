@@ -435,6 +435,140 @@ VDM_API vdm_status vdm_extract_surface(const float* d_f, int32_t R, float* d_ver
  * tri[256][5][3] their edge ids.                                            */
 VDM_API vdm_status vdm_surface_case_table(uint8_t* ntri, uint8_t* tri);
 
+/* ------------------------------------------------------------------ token-sequence operators
+ * Attention-side operators around sets and sequences of tokens: what produces a
+ * vecset before vdm_precompute_kv (self-attention over token sets of different
+ * sizes, normalised and rotated heads) and what keeps many of them (a paged,
+ * optionally 8-bit cache of keys and values, and the attention that reads it).
+ * They have no counterpart on the pages.  Common rules:
+ *   - Asynchronous on `stream`, no host round trip, no allocation: every call
+ *     may be captured into a CUDA graph.  Calls share no state but the error
+ *     word below; each call needs a workspace of its own while it runs.
+ *   - Head tensors are [tokens][heads][D] views (vdm_heads): the D elements of a
+ *     row are contiguous, rows start on 16-byte boundaries (base pointer and
+ *     strides), and rows do not overlap.  D is 64 or 128; dtype f32 or bf16.
+ *   - Sequence b owns the tokens [cu[b], cu[b+1]) of a packed tensor (cu: B+1
+ *     int32, device).  Tokens outside every sequence (behind cu[B]) are neither
+ *     read nor written.  Offsets are clamped to [0, T]; a decreasing pair is an
+ *     empty sequence.  Nothing else about them is checked.
+ *   - Sums, norms and softmax statistics are float32.                       */
+typedef struct {
+    void* data;              /* element [0][0][0]                                */
+    int64_t stride_token;    /* in elements; ignored with one token              */
+    int64_t stride_head;     /* in elements; ignored with one head               */
+} vdm_heads;
+
+/* Rotary position: pair i of a head's first rot_dim elements is turned by
+ * positions[t] * inv_freq[i] and scaled by mscale; elements from rot_dim on pass
+ * through.  The table decides base and long-context scaling.  Angles are reduced
+ * in float64, so far positions keep float32 accuracy.                       */
+typedef struct {
+    int32_t rot_dim;         /* even, 2..D                                       */
+    int32_t interleaved;     /* 1: pairs (2i, 2i+1); 0: (i, i + rot_dim/2)       */
+    const double* inv_freq;  /* device [rot_dim/2], radians per position         */
+    float mscale;            /* factor of the rotated part (1: none)             */
+} vdm_rope;
+
+/* RMS norm of every query and key head, then the rotary position, one pass:
+ *   y = x / sqrt(mean(x^2) + eps) * gain   (gain NULL: that side is not normalised)
+ *   (y_a, y_b) -> mscale (y_a cos - y_b sin, y_a sin + y_b cos)   (rope NULL: none)
+ *   q, q_out [T][Hq][D], k, k_out [T][Hk][D] in dtype (Hk = 0: no keys); an output
+ *   may be its own input.  gains float32 [D]; d_positions int32 [T] (with rope).
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA.                                   */
+VDM_API vdm_status vdm_qk_norm_rope(vdm_dtype dtype, int64_t T, int32_t Hq, int32_t Hk, int32_t D,
+                                    const vdm_heads* q, const vdm_heads* k, const float* d_q_gain,
+                                    const float* d_k_gain, float eps, const vdm_rope* rope,
+                                    const int32_t* d_positions, const vdm_heads* q_out,
+                                    const vdm_heads* k_out, vdm_stream stream);
+
+/* A paged cache of keys and values.  Position p of sequence b lives in page
+ * table[b][p / page_size], row p % page_size (tables int32 [B][max_pages], device).
+ * A table entry outside [0, num_pages) is no page: writes to it are dropped and
+ * it reads as zeros.  Positions from max_pages * page_size on do not exist:
+ * sequence lengths are clamped to that.                                     */
+typedef enum { VDM_CACHE_F32 = 0, VDM_CACHE_BF16 = 1, VDM_CACHE_E4M3 = 2 } vdm_cache_dtype;
+typedef struct {
+    vdm_cache_dtype dtype;
+    int32_t num_pages, page_size;   /* page_size 16, 32, 64, 128 or 256          */
+    int32_t H, D;
+    void *k, *v;                    /* [num_pages][H][page_size][D]              */
+    /* E4M3 only: one scale 2^(s - 127) per row, [num_pages][H][page_size] bytes  */
+    uint8_t *k_scale, *v_scale;
+} vdm_kv_cache;
+
+/* The new tokens of every sequence into the cache: token i of sequence b's n =
+ * cu[b+1] - cu[b] goes to position kv_len[b] - n + i (kv_len counts them;
+ * positions outside the table's reach are dropped).
+ *   k, v [T][H][D] in dtype; the cache holds the same dtype or E4M3.
+ * E4M3: a row (one token and head) gets the smallest e in [-100, 119] with
+ * max |x| <= 448 * 2^e (e = 0 for a zero row), is stored as round(x * 2^-e) to
+ * nearest even, and s = e + 127; infinities and NaN become NaN and do not count
+ * in the maximum.  Reading back is exact: a code times a power of two.
+ * Pages that are written must belong to one sequence (a page that two sequences
+ * write holds some mixture of the two).
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA.                                   */
+VDM_API vdm_status vdm_cache_write(const vdm_kv_cache* cache, vdm_dtype dtype, const vdm_heads* k,
+                                   const vdm_heads* v, int64_t T, const int32_t* d_cu,
+                                   const int32_t* d_kv_len, const int32_t* d_table, int32_t max_pages,
+                                   int32_t B, vdm_stream stream);
+
+/* Back out of the cache: position p < min(kv_len[b], cu[b+1] - cu[b]) of sequence b
+ * to token cu[b] + p of k and v [T][H][D] (dtype: the cache's own, or either for
+ * E4M3; bf16 values beyond its range round as a conversion does).  With the
+ * strides of one shape's [H][N][64] arrays the result is what vdm_decode_dense
+ * reads.  Tokens that no position goes to are left as they were.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA.                                   */
+VDM_API vdm_status vdm_cache_read(const vdm_kv_cache* cache, vdm_dtype dtype, const int32_t* d_kv_len,
+                                  const int32_t* d_table, int32_t max_pages, const int32_t* d_cu,
+                                  int32_t B, int64_t T, const vdm_heads* k, const vdm_heads* v,
+                                  vdm_stream stream);
+
+/* Attention with grouped heads: query head h reads key/value head h / (Hq / Hk).
+ *   out = softmax(scale q k^T) v over the keys a query sees; lse = log of the sum of
+ *   exp(scale q k^T) over them.
+ * causal: query i of n sees keys j <= m - n + i of its sequence's m (the last
+ * query sees all).  A query that sees no key gets out = 0 and lse = -inf; keys
+ * that a query does not see have no influence on it, whatever they hold.  bf16:
+ * the exponentials are rounded to bf16 for the product with v (their sum is not).*/
+typedef struct {
+    int32_t Hq, Hk, D;       /* Hq % Hk == 0                                     */
+    vdm_dtype dtype;         /* of q, out and (packed) k, v                      */
+    int32_t causal;
+    float scale;             /* > 0                                              */
+} vdm_attention;
+
+/* Workspace of either attention call: Tq query tokens in B sequences, no sequence
+ * with more than max_kv keys (packed: Tk; paged: max_pages * page_size).     */
+VDM_API vdm_status vdm_attention_workspace_size(const vdm_attention* a, int32_t B, int64_t Tq, int64_t max_kv,
+                                                size_t* bytes);
+
+/* Packed sequences: queries of sequence b are tokens [cu_q[b], cu_q[b+1]) of q
+ * [Tq][Hq][D], its keys tokens [cu_k[b], cu_k[b+1]) of k and v [Tk][Hk][D].
+ *   out [Tq][Hq][D] in dtype;  d_lse [Tq][Hq] float32 or NULL
+ *   d_ws/ws_bytes  device workspace >= vdm_attention_workspace_size(a, B, Tq, Tk),
+ *                  256-byte aligned
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA.                        */
+VDM_API vdm_status vdm_attention_packed(const vdm_attention* a, const vdm_heads* q, const vdm_heads* k,
+                                        const vdm_heads* v, const int32_t* d_cu_q, const int32_t* d_cu_k,
+                                        int32_t B, int64_t Tq, int64_t Tk, const vdm_heads* out,
+                                        float* d_lse, void* d_ws, size_t ws_bytes, vdm_stream stream);
+
+/* A chunk of new tokens (or one) per sequence over a paged cache that holds them
+ * already: queries of sequence b are tokens [cu_q[b], cu_q[b+1]) of q, its keys
+ * positions [0, kv_len[b]).  The cache's H and D are the call's Hk and D; its
+ * dtype is the call's or E4M3.  Workspace as above with max_kv = max_pages *
+ * page_size.  Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA.             */
+VDM_API vdm_status vdm_attention_paged(const vdm_attention* a, const vdm_heads* q, const vdm_kv_cache* cache,
+                                       const int32_t* d_cu_q, const int32_t* d_kv_len,
+                                       const int32_t* d_table, int32_t max_pages, int32_t B, int64_t Tq,
+                                       const vdm_heads* out, float* d_lse, void* d_ws, size_t ws_bytes,
+                                       vdm_stream stream);
+
+/* The tensor-core attention kernels bound every wait on the device; one that gave
+ * up sets an error word (one per device) and its outputs are not valid.  This
+ * call waits for `stream`, then returns and clears it: OK or TIMEOUT (or CUDA).  */
+VDM_API vdm_status vdm_attention_status(vdm_stream stream);
+
 /* Test hook for failure detection (not needed for decoding).  mode n >= 1
  * makes the n-th tensor-core decode launch from now on (1 = the next one)
  * withhold one completion signal, so its warps run into their bounded waits;

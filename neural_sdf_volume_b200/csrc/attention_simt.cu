@@ -1,0 +1,239 @@
+// Attention on the CUDA cores, float32 arithmetic: the kernel of float32 calls, and the
+// joining of split keys.
+//
+// A block takes 64 query rows (query heads of a group beside one another: row = token x
+// group) of one sequence and key head and runs over its keys in tiles of 64 with the running
+// maximum m and sum l of the softmax: o <- o 2^(m - m') + 2^(s - m') v, out = o / l, with
+// the scale and log2 e folded into s.  Thread (ty, tx) of 16 x 16 owns rows 4 ty .. 4 ty + 3 and
+// keys tx + 16 j of the scores, and columns 4 tx + 64 j of the output: 64 fused multiply-adds
+// per eight 16-byte shared loads.  Bound by the FMA pipe.
+//
+// A key that a row does not see has score -inf and weight 0; since 0 * NaN would still reach
+// the row through the product with v, a value row that not every row of the tile may see is
+// multiplied only where the weight is the row's own (see MASKED).
+#include "seq_internal.cuh"
+
+namespace vdm {
+namespace {
+
+constexpr int BR = 64, BK = 64, ST = 256;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+template <typename T, typename TC, int D, bool PAGED>
+__global__ void __launch_bounds__(ST, 2) attention_simt_kernel(const AttnArgs a) {
+    constexpr int LD = D + 4, LP = BK + 4, NC = D / 64;
+    extern __shared__ float4 smem4[];
+    float* Qs = reinterpret_cast<float*>(smem4);
+    float* Ks = Qs + BR * LD;
+    float* Vs = Ks + BK * LD;
+    float* Ps = Ks;   // the weights replace the keys once every score of the tile is computed
+    RowTile t;
+    if (!find_tile(a, blockIdx.x, BR, a.causal, t)) return;
+    const int hk = blockIdx.y, split = blockIdx.z;
+    const KvRows<TC, PAGED> kv{a, t, hk};
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int n_rows = min(BR, (int)((int64_t)t.nq * a.G - t.row0));
+
+    for (int i = tid; i < BR * (D / 4); i += ST) {
+        const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < n_rows) {
+            const int row = t.row0 + r;
+            x = load4f(reinterpret_cast<const T*>(a.q.p + (t.q0 + row / a.G) * a.q.st +
+                                                  (int64_t)(hk * a.G + row % a.G) * a.q.sh) + d);
+        }
+        *reinterpret_cast<float4*>(Qs + r * LD + d) = x;
+    }
+    int seen[4];
+    float m[4], l[4], o[4][NC][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 4 * ty + i;
+        seen[i] = r < n_rows ? keys_seen(a, t, (t.row0 + r) / a.G) : 0;
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][c][e] = 0.f;
+    }
+    // the tile's rows see at most `most` keys, and all of them see the first `least`
+    const int most = keys_seen(a, t, (t.row0 + n_rows - 1) / a.G), least = keys_seen(a, t, t.row0 / a.G);
+    const int n_tiles = (most + BK - 1) / BK, per = (n_tiles + a.splits - 1) / a.splits;
+    const int j_end = min(most, (split + 1) * per * BK);
+    for (int j0 = split * per * BK; j0 < j_end; j0 += BK) {
+        __syncthreads();
+        for (int i = tid; i < BK * (D / 4); i += ST) {
+            const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+            if (j0 + r < most) {
+                x = kv.get(false, j0 + r, d);
+                y = kv.get(true, j0 + r, d);
+            }
+            *reinterpret_cast<float4*>(Ks + r * LD + d) = x;
+            *reinterpret_cast<float4*>(Vs + r * LD + d) = y;
+        }
+        __syncthreads();
+        float s[4][4] = {};
+#pragma unroll 4
+        for (int d = 0; d < D; d += 4) {
+            float4 qv[4], kk[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                qv[i] = *reinterpret_cast<const float4*>(Qs + (4 * ty + i) * LD + d);
+                kk[i] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * i) * LD + d);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s[i][j] = fmaf(qv[i].x, kk[j].x, s[i][j]);
+                    s[i][j] = fmaf(qv[i].y, kk[j].y, s[i][j]);
+                    s[i][j] = fmaf(qv[i].z, kk[j].z, s[i][j]);
+                    s[i][j] = fmaf(qv[i].w, kk[j].w, s[i][j]);
+                }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = j0 + tx + 16 * j < seen[i] ? s[i][j] * a.scale_log2 : -INFINITY;
+                mx = fmaxf(mx, s[i][j]);
+            }
+#pragma unroll
+            for (int w = 1; w < 16; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+            const float mn = fmaxf(m[i], mx), base = mn == -INFINITY ? 0.f : mn;
+            const float f = exp2f(m[i] - base);
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p = exp2f(s[i][j] - base);
+                sum += p;
+                Ps[(4 * ty + i) * LP + tx + 16 * j] = p;
+            }
+#pragma unroll
+            for (int w = 1; w < 16; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+            l[i] = l[i] * f + sum;
+            m[i] = mn;
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][c][e] *= f;
+        }
+        __syncwarp();   // a row's weights are written and read by the same half-warp
+        // MASKED: rows of the tile see different numbers of keys; then a value row counts only
+        // for rows that see it
+        const bool masked = j0 + BK > least;
+#pragma unroll 2
+        for (int j = 0; j < BK; j += 4) {
+            float4 p[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(Ps + (4 * ty + i) * LP + j);
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) {
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    const float4 v = *reinterpret_cast<const float4*>(Vs + (j + jj) * LD + 64 * c + 4 * tx);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float w = jj == 0 ? p[i].x : jj == 1 ? p[i].y : jj == 2 ? p[i].z : p[i].w;
+                        if (masked && j0 + j + jj >= seen[i]) continue;
+                        o[i][c][0] = fmaf(w, v.x, o[i][c][0]);
+                        o[i][c][1] = fmaf(w, v.y, o[i][c][1]);
+                        o[i][c][2] = fmaf(w, v.z, o[i][c][2]);
+                        o[i][c][3] = fmaf(w, v.w, o[i][c][3]);
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 4 * ty + i;
+        if (r >= n_rows) continue;
+        const int row = t.row0 + r;
+        const int64_t tok = t.q0 + row / a.G;
+        const int h = hk * a.G + row % a.G;
+        const float inv = l[i] == 0.f ? 0.f : 1.0f / l[i];
+        const float lse2 = l[i] == 0.f ? -INFINITY : m[i] + log2f(l[i]);
+        const int64_t prow = ((int64_t)split * a.Tq + tok) * a.Hq + h;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const float4 v = make_float4(o[i][c][0] * inv, o[i][c][1] * inv, o[i][c][2] * inv, o[i][c][3] * inv);
+            const int d = 64 * c + 4 * tx;
+            if (a.splits > 1) store4(a.part_o + prow * D + d, v);
+            else store4(reinterpret_cast<T*>(a.out.p + tok * a.out.st + h * a.out.sh) + d, v);
+        }
+        if (tx == 0) {
+            if (a.splits > 1) a.part_lse[prow] = lse2;
+            else if (a.lse) a.lse[tok * a.Hq + h] = lse2 * kLn2;
+        }
+    }
+}
+
+// Joins the splits of a query row: weights 2^(lse_s - max) over their sum.  One warp per row;
+// the splits are added in order, so the result does not depend on which block ended first.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) combine_kernel(const AttnArgs a) {
+    const int lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5), rows = a.Tq * a.Hq;
+    if (row >= rows) return;
+    const int64_t tok = row / a.Hq;
+    const int h = (int)(row % a.Hq);
+    if (tok < max(a.cu_q[0], 0) || tok >= a.cu_q[a.B]) return;   // behind the last sequence: as it was
+    float mx = -INFINITY;
+    for (int s = 0; s < a.splits; ++s) mx = fmaxf(mx, a.part_lse[s * rows + row]);
+    const float base = mx == -INFINITY ? 0.f : mx;
+    float sum = 0.f, o[D / 32] = {};
+    for (int s = 0; s < a.splits; ++s) {
+        const float lse = a.part_lse[s * rows + row];
+        if (lse == -INFINITY) continue;   // no key: its part holds zeros
+        const float w = exp2f(lse - base);
+        sum += w;
+        const float* p = a.part_o + (s * rows + row) * D;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) o[e] = fmaf(w, p[lane + 32 * e], o[e]);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+    T* out = reinterpret_cast<T*>(a.out.p + tok * a.out.st + h * a.out.sh);
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) out[lane + 32 * e] = from_f<T>(o[e] * inv);
+    if (a.lse && lane == 0) a.lse[row] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * kLn2;
+}
+
+template <typename T, typename TC, int D, bool PAGED>
+vdm_status launch(const AttnArgs& a, cudaStream_t s) {
+    const size_t smem = (size_t)3 * 64 * (D + 4) * 4;
+    auto kern = attention_simt_kernel<T, TC, D, PAGED>;
+    VDM_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+    const int64_t tiles = (a.Tq * a.G + (a.B < a.Tq ? a.B : a.Tq) * (int64_t)(BR - 1)) / BR;
+    kern<<<dim3((unsigned)tiles, a.Hk, a.splits), ST, smem, s>>>(a);
+    VDM_TRY(check_launch("attention_simt_kernel"));
+    return a.splits > 1 ? launch_combine(a, sizeof(T) == 4 ? VDM_F32 : VDM_BF16, s) : VDM_OK;
+}
+
+template <typename T, typename TC>
+vdm_status launch_d(const AttnArgs& a, cudaStream_t s) {
+    if (a.paged) return a.D == 64 ? launch<T, TC, 64, true>(a, s) : launch<T, TC, 128, true>(a, s);
+    if constexpr (sizeof(TC) > 1) return a.D == 64 ? launch<T, TC, 64, false>(a, s) : launch<T, TC, 128, false>(a, s);
+    return fail(VDM_ERR_INTERNAL, "packed keys are not 8-bit");
+}
+
+}  // namespace
+
+vdm_status launch_attention_simt(const AttnArgs& a, vdm_dtype dt, cudaStream_t s) {
+    const bool q8 = a.paged && a.c.dtype == VDM_CACHE_E4M3;
+    if (dt == VDM_F32) return q8 ? launch_d<float, uint8_t>(a, s) : launch_d<float, float>(a, s);
+    return q8 ? launch_d<__nv_bfloat16, uint8_t>(a, s) : launch_d<__nv_bfloat16, __nv_bfloat16>(a, s);
+}
+
+vdm_status launch_combine(const AttnArgs& a, vdm_dtype dt, cudaStream_t s) {
+    const unsigned g = (unsigned)((a.Tq * a.Hq + 3) / 4);
+    if (dt == VDM_F32) a.D == 64 ? combine_kernel<float, 64><<<g, 128, 0, s>>>(a) : combine_kernel<float, 128><<<g, 128, 0, s>>>(a);
+    else a.D == 64 ? combine_kernel<__nv_bfloat16, 64><<<g, 128, 0, s>>>(a) : combine_kernel<__nv_bfloat16, 128><<<g, 128, 0, s>>>(a);
+    return check_launch("combine_kernel");
+}
+
+}  // namespace vdm

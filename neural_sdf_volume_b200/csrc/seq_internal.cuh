@@ -1,0 +1,195 @@
+// Internal declarations of the token-sequence operators (not part of the ABI).
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "vdm_internal.cuh"
+
+namespace vdm {
+
+// a [tokens][heads][D] view, strides in bytes
+struct HeadView {
+    char* p;
+    int64_t st, sh;
+};
+
+struct CacheView {
+    char *k, *v;
+    uint8_t *ks, *vs;       // E4M3: one scale byte per row, else NULL
+    int num_pages, page_size, page_shift, H, D;
+    int dtype;              // vdm_cache_dtype
+    const int32_t* table;   // [B][max_pages]
+    int max_pages;
+};
+
+struct AttnArgs {
+    HeadView q, out, k, v;   // k, v: packed only
+    CacheView c;             // paged only
+    const int32_t* cu_q;
+    const int32_t* cu_k;     // packed: offsets; paged: lengths
+    int paged;
+    int B, Hq, Hk, G, D, causal;
+    int64_t Tq, Tk;
+    float scale_log2;        // softmax scale times log2 e
+    float* lse;              // [Tq][Hq] or NULL
+    // keys split over `splits` blocks: partial results (normalised rows and log2 of their sums)
+    int splits;
+    float* part_o;           // [splits][Tq][Hq][D]
+    float* part_lse;         // [splits][Tq][Hq]
+    int* err;                // error word of bounded waits
+    long long timeout;
+};
+
+// One block of query rows of one sequence and key head.  Rows are (token, query head of the
+// group) with the head fastest: row r is token r / G, head hk * G + r % G.
+struct RowTile {
+    int b;
+    int64_t q0, k0;    // first query token / first key token (packed)
+    int nq, nk;        // query tokens and keys of the sequence
+    int row0;          // first row of the tile
+};
+
+__device__ __forceinline__ int clamp_len(int64_t lo, int64_t hi, int64_t T, int64_t* start) {
+    lo = lo < 0 ? 0 : lo > T ? T : lo;
+    hi = hi < lo ? lo : hi > T ? T : hi;
+    *start = lo;
+    return (int)(hi - lo);
+}
+
+__device__ __forceinline__ int cache_len(const CacheView& c, int32_t len) {
+    const int64_t cap = (int64_t)c.max_pages * c.page_size;
+    return len < 0 ? 0 : len > cap ? (int)cap : len;
+}
+
+// Tile `idx` of the sequences' row tiles of M rows (whole warps, converged); false: no such tile.
+// With `last_first` a sequence's tiles come in descending order (causal: longest first).
+__device__ __forceinline__ bool find_tile(const AttnArgs& a, int64_t idx, int M, bool last_first, RowTile& t) {
+    const int lane = threadIdx.x & 31;
+    int64_t done = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const int b = b0 + lane;
+        int64_t start = 0;
+        int n = 0;
+        if (b < a.B) n = clamp_len(a.cu_q[b], a.cu_q[b + 1], a.Tq, &start);
+        const int64_t tiles = ((int64_t)n * a.G + M - 1) / M;
+        int64_t incl = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        const uint32_t m = __ballot_sync(0xffffffffu, done + incl > idx);
+        if (m) {
+            const int src = __ffs(m) - 1;
+            const int64_t before = done + __shfl_sync(0xffffffffu, incl - tiles, src);
+            const int64_t cnt = __shfl_sync(0xffffffffu, tiles, src);
+            t.b = b0 + src;
+            t.nq = __shfl_sync(0xffffffffu, n, src);
+            t.q0 = __shfl_sync(0xffffffffu, start, src);
+            const int64_t local = idx - before;
+            t.row0 = (int)((last_first ? cnt - 1 - local : local) * M);
+            t.k0 = 0;
+            if (a.paged) t.nk = cache_len(a.c, a.cu_k[t.b]);
+            else t.nk = clamp_len(a.cu_k[t.b], a.cu_k[t.b + 1], a.Tk, &t.k0);
+            return true;
+        }
+        done += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return false;
+}
+
+// keys that query token i of the tile's sequence sees: [0, result)
+__device__ __forceinline__ int keys_seen(const AttnArgs& a, const RowTile& t, int i) {
+    if (!a.causal) return t.nk;
+    const int64_t lim = (int64_t)t.nk - t.nq + i + 1;
+    return lim < 0 ? 0 : (int)lim;
+}
+
+// row of position j of sequence b, head h in the cache, or -1 where there is no page
+__device__ __forceinline__ int64_t cache_row(const CacheView& c, int b, int h, int j) {
+    const int32_t page = c.table[(int64_t)b * c.max_pages + (j >> c.page_shift)];
+    if (page < 0 || page >= c.num_pages) return -1;
+    return (((int64_t)page * c.H + h) << c.page_shift) + (j & (c.page_size - 1));
+}
+
+__device__ __forceinline__ float scale_of(uint8_t s) {
+    // 2^(s - 127); s = 0 never comes from vdm_cache_write and stands for 2^-127
+    return s ? __uint_as_float((uint32_t)s << 23) : __uint_as_float(0x00400000u);
+}
+
+// two e4m3 codes as floats (exact)
+__device__ __forceinline__ float2 e4m3x2_to_f(uint16_t u) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(u, __NV_E4M3);
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// 4 consecutive elements as floats
+__device__ __forceinline__ float4 load4f(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4f(const __nv_bfloat16* p) { return load4(p); }
+__device__ __forceinline__ float4 load4f(const uint8_t* p) {
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
+    const float2 a = e4m3x2_to_f((uint16_t)u), b = e4m3x2_to_f((uint16_t)(u >> 16));
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+    __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    uint2 u;
+    u.x = *reinterpret_cast<uint32_t*>(&a);
+    u.y = *reinterpret_cast<uint32_t*>(&b);
+    *reinterpret_cast<uint2*>(p) = u;
+}
+
+// rows of one key head of the tile's sequence
+template <typename TC, bool PAGED>
+struct KvRows {
+    const AttnArgs& a;
+    const RowTile& t;
+    int hk;
+    // elements [d, d + 4) of key (or value) j, dequantised
+    __device__ __forceinline__ float4 get(bool value, int j, int d) const {
+        if (PAGED) {
+            const int64_t r = cache_row(a.c, t.b, hk, j);
+            if (r < 0) return make_float4(0.f, 0.f, 0.f, 0.f);
+            float4 x = load4f(reinterpret_cast<const TC*>(value ? a.c.v : a.c.k) + r * a.D + d);
+            if (sizeof(TC) == 1) {
+                const float s = scale_of(value ? a.c.vs[r] : a.c.ks[r]);
+                x.x *= s, x.y *= s, x.z *= s, x.w *= s;
+            }
+            return x;
+        }
+        const HeadView& h = value ? a.v : a.k;
+        return load4f(reinterpret_cast<const TC*>(h.p + (t.k0 + j) * h.st + hk * h.sh) + d);
+    }
+};
+
+// launchers
+vdm_status launch_attention_simt(const AttnArgs& a, vdm_dtype dt, cudaStream_t s);
+vdm_status launch_combine(const AttnArgs& a, vdm_dtype dt, cudaStream_t s);
+int attention_splits(const vdm_attention* a, int B, int64_t Tq, int64_t max_kv);
+
+struct RopeArgs {
+    int64_t T;
+    int Hq, Hk, D;
+    HeadView q, k, qo, ko;
+    const float *gq, *gk;
+    float eps;
+    int rot, interleaved;
+    const double* inv_freq;
+    float mscale;
+    const int32_t* pos;
+};
+vdm_status launch_qk_norm_rope(const RopeArgs& a, vdm_dtype dt, cudaStream_t s);
+
+struct CacheIo {
+    CacheView c;
+    HeadView k, v;
+    const int32_t *cu, *kv_len;
+    int B;
+    int64_t T;
+};
+vdm_status launch_cache_write(const CacheIo& a, vdm_dtype dt, cudaStream_t s);
+vdm_status launch_cache_read(const CacheIo& a, vdm_dtype dt, cudaStream_t s);
+
+}  // namespace vdm
