@@ -3,10 +3,26 @@
 #include <math.h>
 #include <string.h>
 
+#include <atomic>
+
 #include "seq_internal.cuh"
 
 namespace vdm {
 namespace {
+
+__device__ int g_attention_error = 0;   // site of the first wait that gave up, 0: none
+
+// its address, asked for once per device
+vdm_status attention_error_word(int** p) {
+    static std::atomic<int*> known[64];
+    int dev = 0;
+    VDM_CUDA_TRY(cudaGetDevice(&dev));
+    *p = dev < 64 ? known[dev].load() : nullptr;
+    if (*p) return VDM_OK;
+    VDM_CUDA_TRY(cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_attention_error));
+    if (dev < 64) known[dev].store(*p);
+    return VDM_OK;
+}
 
 size_t dtype_size(vdm_dtype d) { return d == VDM_F32 ? 4 : 2; }
 bool al16(const void* p) { return ((uintptr_t)p & 15) == 0; }
@@ -94,6 +110,36 @@ vdm_status check_attention(const vdm_attention* a) {
     return VDM_OK;
 }
 
+// Kernel and number of blocks that share a row tile's keys.  Depends on sizes alone, so that
+// the workspace can be asked for beforehand.
+enum Kernel : int { kSimt, kTc };
+struct Plan {
+    int kernel, splits;
+};
+
+Plan plan_attention(const vdm_attention* at, int B, int64_t Tq, int64_t max_kv) {
+    Plan p;
+    const int64_t G = at->Hq / at->Hk, seqs = B < Tq ? B : Tq;
+    if (seqs == 0) return Plan{kSimt, 1};
+    p.kernel = at->dtype == VDM_F32 ? kSimt : kTc;
+    // Row tiles of the kernel, blocks that run at once, and the cost of a block in key tiles: its
+    // own share of the keys and a start and end worth about two tiles.  The number of splits is
+    // the one with the shortest sum over waves; joining s parts costs about s rows' writing and reading.
+    const int64_t M = p.kernel == kTc ? 256 : 64, N = p.kernel == kTc ? 128 : 64, at_once = p.kernel == kTc ? 148 : 296;
+    const int64_t tiles = (Tq * G + seqs * (M - 1)) / M * at->Hk, nk = (max_kv + N - 1) / N;
+    double best = 0;
+    p.splits = 1;
+    for (int s = 1; s <= 64 && s * 2 <= (nk > 2 ? nk : 2); ++s) {
+        const double waves = (double)((tiles * s + at_once - 1) / at_once);
+        const double cost = waves * ((double)((nk + s - 1) / s) + 2.0) + (s > 1 ? 2.0 + 0.25 * s * waves : 0.0);
+        if (s == 1 || cost < 0.95 * best) {
+            best = cost;
+            p.splits = s;
+        }
+    }
+    return p;
+}
+
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 vdm_status run_attention(const vdm_attention* at, AttnArgs& a, int64_t max_kv, const vdm_heads* out, float* lse, void* ws,
@@ -113,25 +159,17 @@ vdm_status run_attention(const vdm_attention* at, AttnArgs& a, int64_t max_kv, c
     if (need && (!ws || ws_bytes < need))
         return fail(VDM_ERR_WORKSPACE, "attention: workspace of %zu bytes, %zu needed", ws ? ws_bytes : (size_t)0, need);
     if (need && ((uintptr_t)ws & 255)) return fail(VDM_ERR_INVALID_ARG, "attention: workspace must be 256-byte aligned");
-    a.splits = attention_splits(at, a.B, a.Tq, max_kv);
+    const Plan plan = plan_attention(at, a.B, a.Tq, max_kv);
+    a.splits = plan.splits;
     a.part_o = static_cast<float*>(ws);
     a.part_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + up256((size_t)a.splits * a.Tq * at->Hq * at->D * 4));
-    return launch_attention_simt(a, at->dtype, reinterpret_cast<cudaStream_t>(stream));
+    VDM_TRY(attention_error_word(&a.err));
+    a.timeout = 4000000000ll;   // cycles of one bounded wait, about two seconds
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return plan.kernel == kTc ? launch_attention_tc(a, st) : launch_attention_simt(a, at->dtype, st);
 }
 
 }  // namespace
-
-// Blocks that share a row tile's keys: as many as fill the GPU twice with blocks, as long as
-// each has 256 keys at least.
-int attention_splits(const vdm_attention* at, int B, int64_t Tq, int64_t max_kv) {
-    const int64_t G = at->Hq / at->Hk, M = 64;
-    const int64_t seqs = B < Tq ? B : Tq;
-    const int64_t tiles = (Tq * G + seqs * (M - 1)) / M * at->Hk;
-    if (tiles == 0) return 1;
-    const int64_t want = 296 / tiles, most = max_kv / 256;
-    const int64_t s = want < most ? want : most;
-    return s < 1 ? 1 : s > 64 ? 64 : (int)s;
-}
 
 }  // namespace vdm
 
@@ -209,7 +247,7 @@ vdm_status vdm_attention_workspace_size(const vdm_attention* at, int32_t B, int6
     VDM_TRY(check_attention(at));
     VDM_TRY(check_count("attention", Tq, B));
     if (max_kv < 0 || !bytes) return fail(VDM_ERR_INVALID_ARG, "attention: max_kv < 0 or bytes is NULL");
-    const int s = attention_splits(at, B, Tq, max_kv);
+    const int s = plan_attention(at, B, Tq, max_kv).splits;
     *bytes = s < 2 ? 0 : up256((size_t)s * Tq * at->Hq * at->D * 4) + up256((size_t)s * Tq * at->Hq * 4);
     return VDM_OK;
 }
@@ -253,8 +291,16 @@ vdm_status vdm_attention_paged(const vdm_attention* at, const vdm_heads* q, cons
 }
 
 vdm_status vdm_attention_status(vdm_stream stream) {
-    VDM_CUDA_TRY(cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)));
-    return VDM_OK;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    int* word = nullptr;
+    VDM_TRY(attention_error_word(&word));
+    int site = 0;
+    VDM_CUDA_TRY(cudaMemcpyAsync(&site, word, sizeof(int), cudaMemcpyDeviceToHost, s));
+    VDM_CUDA_TRY(cudaStreamSynchronize(s));
+    if (!site) return VDM_OK;
+    VDM_CUDA_TRY(cudaMemsetAsync(word, 0, sizeof(int), s));
+    VDM_CUDA_TRY(cudaStreamSynchronize(s));
+    return fail(VDM_ERR_TIMEOUT, "attention: bounded wait expired at site %d", site);
 }
 
 }  // extern "C"

@@ -166,8 +166,8 @@ struct KvRows {
 
 // launchers
 vdm_status launch_attention_simt(const AttnArgs& a, vdm_dtype dt, cudaStream_t s);
+vdm_status launch_attention_tc(const AttnArgs& a, cudaStream_t s);
 vdm_status launch_combine(const AttnArgs& a, vdm_dtype dt, cudaStream_t s);
-int attention_splits(const vdm_attention* a, int B, int64_t Tq, int64_t max_kv);
 
 struct RopeArgs {
     int64_t T;
