@@ -512,77 +512,18 @@ def vdm_refine_level(f, fine=None, parents=None, workspace=None, stream=None):
 # result).  Sequence b owns tokens cu[b] .. cu[b+1] - 1.  The calls return without waiting.
 PAGE_SIZES = (16, 32, 64, 128, 256)
 
-
-class _On:
-    """The device of a call's tensors made current, and its stream: ``stream`` or
-    that device's current one.  What a call allocates belongs to that stream."""
-
-    __slots__ = ("stream", "_guards")
-
-    def __init__(self, torch, device, stream):
-        self._guards = ()
-        if device.index != torch.cuda.current_device():
-            self._guards += (torch.cuda.device(device),)
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError(f"the stream is of {stream.device}, the tensors of {device}")
-            self._guards += (torch.cuda.stream(stream),)
-        self.stream = stream.cuda_stream if stream is not None else torch.cuda.current_stream(device).cuda_stream
-
-    def __enter__(self):
-        for g in self._guards:
-            g.__enter__()
-        return self.stream
-
-    def __exit__(self, *exc):
-        for g in reversed(self._guards):
-            g.__exit__(*exc)
+_native = None
 
 
-def _device_of(name, t):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (got one on {t.device})")
-    return t.device
-
-
-def _seq_dtype(name, t):
-    torch = _torch()
-    if t.dtype is torch.bfloat16:
-        return VDM_BF16
-    if t.dtype is torch.float32:
-        return VDM_F32
-    raise ValueError(f"{name} must be bfloat16 or float32 (got {t.dtype})")
-
-
-def _heads(name, t, device, dtype, T=None, H=None, D=None):
-    """``vdm_heads`` of a [tokens, heads, D] tensor, after checking it against the call's sizes."""
-    if t.dim() != 3 or (T is not None and t.shape[0] != T) or (H is not None and t.shape[1] != H) or \
-            (D is not None and t.shape[2] != D):
-        want = [x if x is not None else "*" for x in (T, H, D)]
-        raise ValueError(f"{name} must have shape {want} (got {list(t.shape)})")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
-    st, sh, se = t.stride()
-    if se != 1 and t.numel():
-        raise ValueError(f"{name}: the elements of a head must be contiguous (stride {se})")
-    return CHeads(t.data_ptr(), st, sh)
-
-
-def _index(name, t, device, *shape):
-    """Pointer of a contiguous int32 device tensor of the given shape."""
-    torch = _torch()
-    if t.dtype is not torch.int32 or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)} on {device} "
-                         f"(got {t.dtype}, {list(t.shape)}, {t.device})")
-    return t.data_ptr()
-
-
-def _sequences(name, cu):
-    if cu.dim() != 1 or cu.shape[0] < 1:
-        raise ValueError(f"{name} must hold B + 1 offsets (got shape {list(cu.shape)})")
-    return cu.shape[0] - 1
+def _load_seq():
+    """The native module of these calls (``csrc/seq_binding.cpp``), loaded with torch at the first of them."""
+    global _native
+    if _native is None:
+        import torch  # noqa: F401  (its libraries first)
+        from . import _seq as native
+        native.set_check(_check)
+        _native = native
+    return _native
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, factor: float = 1.0, original_length: int = 0,
@@ -623,35 +564,7 @@ def vdm_qk_norm_rope(q, k=None, positions=None, rope: Optional[Rope] = None, q_g
     """RMS norm of every head of ``q[T,Hq,D]`` and ``k[T,Hk,D]`` (gains float32 [D]; a side
     without one is not normalised), then the rotary position ``positions[T]`` (int32), in one
     pass: ``(q_out, k_out)``.  Outputs may be the inputs; without ``k``, ``k_out`` is None."""
-    torch = _torch()
-    dev, dt = _device_of("q", q), _seq_dtype("q", q)
-    T, Hq, D = q.shape if q.dim() == 3 else (None, None, None)
-    hq = _heads("q", q, dev, q.dtype)
-    Hk, hk, hko = 0, None, None
-    if k is not None:
-        hk = _heads("k", k, dev, q.dtype, T, None, D)
-        Hk = k.shape[1]
-    for name, g in (("q_gain", q_gain), ("k_gain", k_gain)):
-        if g is not None and (g.dtype is not torch.float32 or tuple(g.shape) != (D,) or g.device != dev or not g.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous float32 tensor of shape [{D}] on {dev}")
-    cr, pos = None, None
-    if rope is not None:
-        f = rope.inv_freq
-        if f.dtype is not torch.float64 or f.dim() != 1 or f.device != dev or not f.is_contiguous():
-            raise ValueError(f"rope.inv_freq must be a contiguous float64 tensor [rot_dim/2] on {dev}")
-        if positions is None:
-            raise ValueError("a rotation needs positions")
-        cr, pos = CRope(2 * f.shape[0], int(rope.interleaved), f.data_ptr(), rope.mscale), _index("positions", positions, dev, T)
-    with _On(torch, dev, stream) as s:
-        if q_out is None:
-            q_out = torch.empty((T, Hq, D), device=dev, dtype=q.dtype)
-        hqo = _heads("q_out", q_out, dev, q.dtype, T, Hq, D)
-        if k is not None:
-            if k_out is None:
-                k_out = torch.empty((T, Hk, D), device=dev, dtype=q.dtype)
-            hko = _heads("k_out", k_out, dev, q.dtype, T, Hk, D)
-        _check(_lib.vdm_qk_norm_rope(dt, T, Hq, Hk, D, hq, hk, _ptr(q_gain), _ptr(k_gain), eps, cr, pos, hqo, hko, s))
-    return q_out, k_out if k is not None else None
+    return (_native or _load_seq()).qk_norm_rope(q, k, positions, rope, q_gain, k_gain, eps, q_out, k_out, stream)
 
 
 @dataclass
@@ -701,55 +614,27 @@ class KVCache:
         return c
 
 
-def _cache_args(cache, table, kv_len, cu, dev):
-    B = _sequences("cu", cu)
-    if cache.k.device != dev:
-        raise ValueError(f"the cache is on {cache.k.device}, the call's other tensors on {dev}")
-    if table.dim() != 2:
-        raise ValueError(f"table must be [B, max_pages] (got {list(table.shape)})")
-    return B, _index("cu", cu, dev, B + 1), _index("kv_len", kv_len, dev, B), _index("table", table, dev, B, table.shape[1])
-
-
 def vdm_cache_write(cache: KVCache, k, v, cu, kv_len, table, stream=None):
     """New tokens ``k, v [T,H,D]`` of the sequences ``cu[B+1]`` into the cache: the last positions
     of ``kv_len[B]`` tokens (the new ones counted), in the pages ``table[B, max_pages]``."""
-    torch = _torch()
-    dev, dt = _device_of("k", k), _seq_dtype("k", k)
-    cc = cache.cstruct()
-    T = k.shape[0] if k.dim() else 0
-    B, pcu, plen, ptab = _cache_args(cache, table, kv_len, cu, dev)
-    hk = _heads("k", k, dev, k.dtype, T, cc.H, cc.D)
-    hv = _heads("v", v, dev, k.dtype, T, cc.H, cc.D)
-    with _On(torch, dev, stream) as s:
-        _check(_lib.vdm_cache_write(cc, dt, hk, hv, T, pcu, plen, ptab, table.shape[1], B, s))
+    (_native or _load_seq()).cache_write(cache, k, v, cu, kv_len, table, stream)
 
 
 def vdm_cache_read(cache: KVCache, kv_len, table, cu, total: Optional[int] = None, dtype=None, out=None, stream=None):
     """The cached tokens of every sequence, packed by ``cu``: ``(k, v)`` ``[total,H,D]`` (``dtype``:
     by default the cache's own, bfloat16 of an 8-bit one), or into ``out = (k, v)``."""
-    torch = _torch()
-    cc = cache.cstruct()
-    dev = _device_of("cache.k", cache.k)
-    B, pcu, plen, ptab = _cache_args(cache, table, kv_len, cu, dev)
-    with _On(torch, dev, stream) as s:
-        if out is None:
-            if total is None:
-                raise ValueError("cache_read needs the number of tokens (total) or out")
-            if dtype is None:
-                dtype = torch.bfloat16 if cc.dtype == 2 else cache.k.dtype
-            out = tuple(torch.empty((total, cc.H, cc.D), device=dev, dtype=dtype) for _ in "kv")
-        k, v = out
-        dt = _seq_dtype("out", k)
-        T = k.shape[0] if k.dim() else 0
-        hk = _heads("k", k, dev, k.dtype, T, cc.H, cc.D)
-        hv = _heads("v", v, dev, k.dtype, T, cc.H, cc.D)
-        _check(_lib.vdm_cache_read(cc, dt, plen, ptab, table.shape[1], pcu, B, T, hk, hv, s))
+    if out is None:
+        torch = _torch()
+        if total is None:
+            raise ValueError("cache_read needs the number of tokens (total) or out")
+        cc, t = cache.cstruct(), cache.k
+        if dtype is None:
+            dtype = torch.bfloat16 if cc.dtype == 2 else t.dtype
+        with torch.cuda.stream(stream):          # allocated where the call runs
+            out = tuple(torch.empty((total, cc.H, cc.D), device=t.device, dtype=dtype) for _ in "kv")
+    k, v = out
+    (_native or _load_seq()).cache_read(cache, kv_len, table, cu, k, v, stream)
     return k, v
-
-
-def _attention(q, Hk, causal, scale):
-    T, Hq, D = q.shape
-    return CAttention(Hq, Hk, D, _seq_dtype("q", q), int(bool(causal)), D ** -0.5 if scale is None else scale)
 
 
 def vdm_attention_workspace_size(Hq: int, Hk: int, D: int, dtype: str, B: int, Tq: int, max_kv: int) -> int:
@@ -759,47 +644,13 @@ def vdm_attention_workspace_size(Hq: int, Hk: int, D: int, dtype: str, B: int, T
     return int(n.value)
 
 
-def _attend(ca, q, hq, B, max_kv, dev, out, want_lse, workspace, stream, call):
-    torch = _torch()
-    Tq = q.shape[0]
-    with _On(torch, dev, stream) as s:
-        if out is None:
-            out = torch.empty(q.shape, device=dev, dtype=q.dtype)
-        ho = _heads("out", out, dev, q.dtype, *q.shape)
-        lse = torch.empty((Tq, ca.Hq), device=dev, dtype=torch.float32) if want_lse else None
-        if workspace is None:
-            n = C.c_size_t(0)
-            _check(_lib.vdm_attention_workspace_size(ca, B, Tq, max_kv, n))
-            if n.value:
-                workspace = torch.empty((n.value,), device=dev, dtype=torch.uint8)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-        nb = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _check(call(ho, _ptr(lse), _ptr(workspace), nb, s))
-    return (out, lse) if want_lse else out
-
-
 def vdm_attention_packed(q, k, v, cu_q, cu_k=None, causal: bool = True, scale: Optional[float] = None, out=None,
                          want_lse: bool = False, workspace=None, stream=None):
     """Attention of packed sequences: ``q[Tq,Hq,D]`` to ``k, v [Tk,Hk,D]``, sequence b the tokens
     ``cu_q[b]..`` and ``cu_k[b]..`` (by default the same), query head h to key head ``h // (Hq/Hk)``;
     causal: aligned to the sequences' ends.  ``scale`` defaults to D^-1/2.  Returns ``out`` (rows
     outside every sequence are not written), with ``want_lse`` also the log of the sums ``[Tq,Hq]``."""
-    dev = _device_of("q", q)
-    hq = _heads("q", q, dev, q.dtype)
-    if k.dim() != 3:
-        raise ValueError(f"k must be [tokens, heads, D] (got {list(k.shape)})")
-    Tk, Hk, D = k.shape[0], k.shape[1], q.shape[2]
-    hk = _heads("k", k, dev, q.dtype, Tk, Hk, D)
-    hv = _heads("v", v, dev, q.dtype, Tk, Hk, D)
-    ca = _attention(q, Hk, causal, scale)
-    B = _sequences("cu_q", cu_q)
-    pq = _index("cu_q", cu_q, dev, B + 1)
-    if cu_k is None and Tk != q.shape[0]:
-        raise ValueError("queries and keys of different lengths need cu_k")
-    pk = pq if cu_k is None else _index("cu_k", cu_k, dev, B + 1)
-    return _attend(ca, q, hq, B, Tk, dev, out, want_lse, workspace, stream,
-                   lambda ho, lse, ws, nb, s: _lib.vdm_attention_packed(ca, hq, hk, hv, pq, pk, B, q.shape[0], Tk, ho, lse, ws, nb, s))
+    return (_native or _load_seq()).attention_packed(q, k, v, cu_q, cu_k, causal, scale, out, want_lse, workspace, stream)
 
 
 def vdm_attention_paged(q, cache: KVCache, cu_q, kv_len, table, causal: bool = True, scale: Optional[float] = None,
@@ -807,14 +658,7 @@ def vdm_attention_paged(q, cache: KVCache, cu_q, kv_len, table, causal: bool = T
     """A chunk of new tokens of every sequence (``q[Tq,Hq,D]``, ``cu_q[B+1]``), or a single one, over
     the ``kv_len[B]`` tokens that the cache holds of it, the new ones among them; causal: the last
     query sees all of them.  Otherwise as ``vdm_attention_packed``."""
-    dev = _device_of("q", q)
-    hq = _heads("q", q, dev, q.dtype)
-    cc = cache.cstruct()
-    ca = _attention(q, cc.H, causal, scale)
-    B, pcu, plen, ptab = _cache_args(cache, table, kv_len, cu_q, dev)
-    mp = table.shape[1]
-    return _attend(ca, q, hq, B, mp * cc.page_size, dev, out, want_lse, workspace, stream,
-                   lambda ho, lse, ws, nb, s: _lib.vdm_attention_paged(ca, hq, cc, pcu, plen, ptab, mp, B, q.shape[0], ho, lse, ws, nb, s))
+    return (_native or _load_seq()).attention_paged(q, cache, cu_q, kv_len, table, causal, scale, out, want_lse, workspace, stream)
 
 
 def vdm_attention_status(stream=None):
