@@ -208,9 +208,9 @@ __global__ void __launch_bounds__(RW * 32) attention_rows_kernel(const __grid_co
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
             // exponent e of the maximum (2^e <= mx < 2^(e+1)); Q' = Q 2^(14 - e)
-            const int e = mx > 0.f && mx < INFINITY ? (int)(__float_as_uint(mx) >> 23) - 127 : 14;
-            mul = exp2f((float)min(14 - e, 120));
-            rs[r] = a.scale_log2 * exp2f(-(float)min(14 - e, 120));
+            const int e = mx > 0.f ? (int)(__float_as_uint(mx) >> 23) - 127 : 14, up = min(14 - e, 120);
+            mul = pow2i(up);
+            rs[r] = a.scale_log2 * pow2i(-up);
         }
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
@@ -438,7 +438,8 @@ template <int D, int SRC, bool ROWS8>
 vdm_status launch(const AttnArgs& a, cudaStream_t s) {
     auto kern = attention_rows_kernel<D, SRC, ROWS8>;
     constexpr int M = ROWS8 ? 8 : RM;
-    VDM_TRY(prepare_kernel(reinterpret_cast<const void*>(kern), Cfg<D, SRC>::SMEM, true));
+    static std::atomic<uint64_t> ready{0};
+    VDM_TRY(prepare_kernel(ready, reinterpret_cast<const void*>(kern), Cfg<D, SRC>::SMEM, true));
     const int64_t tiles = (a.Tq * a.G + (a.B < a.Tq ? a.B : a.Tq) * (int64_t)(M - 1)) / M;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)tiles, a.Hk, a.splits * a.cluster);
@@ -465,6 +466,7 @@ vdm_status launch_d(const AttnArgs& a, cudaStream_t s) {
 }  // namespace
 
 vdm_status launch_attention_rows(const AttnArgs& a, cudaStream_t s) {
+    if (a.paged ? a.c.num_pages == 0 || a.c.max_pages == 0 : a.Tk == 0) return launch_attention_simt(a, VDM_BF16, s);   // no keys at all
     if (!a.paged) return launch_d<kPacked>(a, s);
     return a.c.dtype == VDM_CACHE_E4M3 ? launch_d<kPagedE4m3>(a, s) : launch_d<kPagedBf16>(a, s);
 }

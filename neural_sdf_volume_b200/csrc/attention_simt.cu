@@ -207,7 +207,8 @@ template <typename T, typename TC, int D, bool PAGED>
 vdm_status launch(const AttnArgs& a, cudaStream_t s) {
     const size_t smem = (size_t)3 * 64 * (D + 4) * 4;
     auto kern = attention_simt_kernel<T, TC, D, PAGED>;
-    VDM_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+    static std::atomic<uint64_t> ready{0};
+    VDM_TRY(prepare_kernel(ready, reinterpret_cast<const void*>(kern), (int)smem));
     const int64_t tiles = (a.Tq * a.G + (a.B < a.Tq ? a.B : a.Tq) * (int64_t)(BR - 1)) / BR;
     kern<<<dim3((unsigned)tiles, a.Hk, a.splits), ST, smem, s>>>(a);
     VDM_TRY(check_launch("attention_simt_kernel"));

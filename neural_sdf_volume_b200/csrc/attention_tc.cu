@@ -126,38 +126,6 @@ __device__ __forceinline__ void st_v4(uint32_t addr, uint32_t a, uint32_t b, uin
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// One row again over keys [j0, j1) alone, by a whole warp; lane's elements are 4 lane + 0..3 of
-// D = 128 and of D = 64 in its first 16 lanes.  Normalised values in o, result: log2 of the sum.
-template <typename TC, int D, bool PAGED>
-__device__ __noinline__ float repair_row(const AttnArgs& a, const RowTile& t, int hk, int row, int j0, int j1, float4& o) {
-    const int lane = threadIdx.x & 31;
-    const bool on = 4 * lane < D;
-    const KvRows<TC, PAGED> kv{a, t, hk};
-    float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
-    o = q;
-    if (on) q = load4f(reinterpret_cast<const __nv_bfloat16*>(a.q.p + (t.q0 + row / a.G) * a.q.st +
-                                                              (int64_t)(hk * a.G + row % a.G) * a.q.sh) + 4 * lane);
-    float m = -INFINITY, l = 0.f;
-    for (int j = j0; j < j1; ++j) {
-        float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
-        if (on) {
-            k = kv.get(false, j, 4 * lane);
-            v = kv.get(true, j, 4 * lane);
-        }
-        float s = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, q.w * k.w)));
-        for (int w = 16; w; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-        s *= a.scale_log2;
-        const float mn = fmaxf(m, s), base = mn == -INFINITY ? 0.f : mn;
-        const float f = exp2f(m - base), p = exp2f(s - base);
-        m = mn;
-        l = l * f + p;
-        o.x = fmaf(p, v.x, o.x * f), o.y = fmaf(p, v.y, o.y * f), o.z = fmaf(p, v.z, o.z * f), o.w = fmaf(p, v.w, o.w * f);
-    }
-    const float inv = l == 0.f ? 0.f : 1.0f / l;
-    o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
-    return l == 0.f ? -INFINITY : m + log2f(l);
-}
-
 template <int D, int SRC>
 __global__ void __launch_bounds__(SRC == kPagedE4m3 ? 384 : 320, 1)
 attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -561,7 +529,8 @@ vdm_status paged_map(CUtensorMap* m, char* base, const CacheView& c) {
 template <int D, int SRC>
 vdm_status launch(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, bool tok_first, cudaStream_t s) {
     auto kern = attention_tc_kernel<D, SRC>;
-    VDM_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM));
+    static std::atomic<uint64_t> ready{0};
+    VDM_TRY(prepare_kernel(ready, reinterpret_cast<const void*>(kern), Cfg<D>::SMEM));
     const int64_t tiles = (a.Tq * a.G + (a.B < a.Tq ? a.B : a.Tq) * (int64_t)(2 * BM - 1)) / (2 * BM);
     kern<<<dim3((unsigned)tiles, a.Hk, a.splits), SRC == kPagedE4m3 ? 384 : 320, Cfg<D>::SMEM, s>>>(mk, mv, a, tok_first);
     VDM_TRY(check_launch("attention_tc_kernel"));

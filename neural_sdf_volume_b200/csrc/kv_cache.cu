@@ -35,8 +35,6 @@ __device__ __forceinline__ int row_exponent(float m) {
     return e < -100 ? -100 : e > 119 ? 119 : e;
 }
 
-__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-
 // 8 elements as they are (also the bits of a NaN)
 template <typename T>
 __device__ __forceinline__ void copy8(T* d, const T* s) {

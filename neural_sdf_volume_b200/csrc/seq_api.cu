@@ -74,8 +74,8 @@ vdm_status check_cache(const vdm_kv_cache* c, const int32_t* table, int max_page
     if (c->num_pages > 0) {
         if (!c->k || !c->v || !al16(c->k) || !al16(c->v))
             return fail(VDM_ERR_INVALID_ARG, "cache: k and v must be 16-byte aligned device memory");
-        if (c->dtype == VDM_CACHE_E4M3 && (!c->k_scale || !c->v_scale))
-            return fail(VDM_ERR_INVALID_ARG, "cache: an E4M3 cache needs k_scale and v_scale");
+        if (c->dtype == VDM_CACHE_E4M3 && (!c->k_scale || !c->v_scale || !al16(c->k_scale) || !al16(c->v_scale)))
+            return fail(VDM_ERR_INVALID_ARG, "cache: an E4M3 cache needs k_scale and v_scale, 16-byte aligned");
     }
     if (max_pages > 0 && !table) return fail(VDM_ERR_INVALID_ARG, "page table is NULL");
     v->k = static_cast<char*>(c->k);
@@ -112,23 +112,32 @@ vdm_status check_attention(const vdm_attention* a) {
 
 // Kernel and number of blocks that share a row tile's keys.  Depends on sizes alone, so that
 // the workspace can be asked for beforehand.
-enum Kernel : int { kSimt, kTc };
+enum Kernel : int { kSimt, kTc, kRows };
 struct Plan {
-    int kernel, splits;
+    int kernel, splits, cluster;
 };
 
 Plan plan_attention(const vdm_attention* at, int B, int64_t Tq, int64_t max_kv) {
     Plan p;
     const int64_t G = at->Hq / at->Hk, seqs = B < Tq ? B : Tq;
-    if (seqs == 0) return Plan{kSimt, 1};
+    p.splits = p.cluster = 1;
     p.kernel = at->dtype == VDM_F32 ? kSimt : kTc;
+    if (seqs == 0) return p;
+    if (p.kernel == kTc && Tq * G <= 32 * seqs) {
+        p.kernel = kRows;
+        const int64_t M = rows_tile((int)G, Tq, B), tiles = (Tq * G + seqs * (M - 1)) / M * at->Hk;
+        const int64_t steps = (max_kv + 31) / 32;
+        while (p.cluster < 16 && tiles * p.cluster < 2400 && p.cluster * 8 < steps) p.cluster *= 2;
+        if (p.cluster == 16)
+            while (p.splits < 16 && tiles * p.cluster * p.splits < 296 && p.splits * p.cluster * 32 < steps) p.splits *= 2;
+        return p;
+    }
     // Row tiles of the kernel, blocks that run at once, and the cost of a block in key tiles: its
     // own share of the keys and a start and end worth about two tiles.  The number of splits is
     // the one with the shortest sum over waves; joining s parts costs about s rows' writing and reading.
     const int64_t M = p.kernel == kTc ? 256 : 64, N = p.kernel == kTc ? 128 : 64, at_once = p.kernel == kTc ? 148 : 296;
     const int64_t tiles = (Tq * G + seqs * (M - 1)) / M * at->Hk, nk = (max_kv + N - 1) / N;
     double best = 0;
-    p.splits = 1;
     for (int s = 1; s <= 64 && s * 2 <= (nk > 2 ? nk : 2); ++s) {
         const double waves = (double)((tiles * s + at_once - 1) / at_once);
         const double cost = waves * ((double)((nk + s - 1) / s) + 2.0) + (s > 1 ? 2.0 + 0.25 * s * waves : 0.0);
@@ -161,11 +170,13 @@ vdm_status run_attention(const vdm_attention* at, AttnArgs& a, int64_t max_kv, c
     if (need && ((uintptr_t)ws & 255)) return fail(VDM_ERR_INVALID_ARG, "attention: workspace must be 256-byte aligned");
     const Plan plan = plan_attention(at, a.B, a.Tq, max_kv);
     a.splits = plan.splits;
+    a.cluster = plan.cluster;
     a.part_o = static_cast<float*>(ws);
     a.part_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + up256((size_t)a.splits * a.Tq * at->Hq * at->D * 4));
     VDM_TRY(attention_error_word(&a.err));
     a.timeout = 4000000000ll;   // cycles of one bounded wait, about two seconds
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (plan.kernel == kRows) return launch_attention_rows(a, st);
     return plan.kernel == kTc ? launch_attention_tc(a, st) : launch_attention_simt(a, at->dtype, st);
 }
 

@@ -3,6 +3,8 @@
 
 #include <cuda_fp8.h>
 
+#include <atomic>
+
 #include "vdm_internal.cuh"
 
 namespace vdm {
@@ -36,6 +38,7 @@ struct AttnArgs {
     int splits;
     float* part_o;           // [splits][Tq][Hq][D]
     float* part_lse;         // [splits][Tq][Hq]
+    int cluster;             // few rows: blocks that share a tile's keys and join in shared memory
     int* err;                // error word of bounded waits
     long long timeout;
 };
@@ -123,6 +126,8 @@ __device__ __forceinline__ float2 e4m3x2_to_f(uint16_t u) {
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // -126 <= e <= 127
+
 // 4 consecutive elements as floats
 __device__ __forceinline__ float4 load4f(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ float4 load4f(const __nv_bfloat16* p) { return load4(p); }
@@ -164,7 +169,58 @@ struct KvRows {
     }
 };
 
+// One row again over keys [j0, j1) alone, by a whole warp; lane's elements are 4 lane + 0..3 of
+// D = 128 and of D = 64 in its first 16 lanes.  Normalised values in o, result: log2 of the sum.
+// (keys that a row does not see have weight 0, and 0 * NaN or 0 * inf of their values would still
+// reach it through a matrix product: a row that ends up not finite while keys of its tiles were
+// masked is computed by this instead; never called with finite values)
+template <typename TC, int D, bool PAGED>
+__device__ __forceinline__ float repair_row(const AttnArgs& a, const RowTile& t, int hk, int row, int j0, int j1, float4& o) {
+    const int lane = threadIdx.x & 31;
+    const bool on = 4 * lane < D;
+    const KvRows<TC, PAGED> kv{a, t, hk};
+    float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+    o = q;
+    if (on) q = load4f(reinterpret_cast<const __nv_bfloat16*>(a.q.p + (t.q0 + row / a.G) * a.q.st +
+                                                              (int64_t)(hk * a.G + row % a.G) * a.q.sh) + 4 * lane);
+    float m = -INFINITY, l = 0.f;
+    for (int j = j0; j < j1; ++j) {
+        float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
+        if (on) {
+            k = kv.get(false, j, 4 * lane);
+            v = kv.get(true, j, 4 * lane);
+        }
+        float s = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, q.w * k.w)));
+        for (int w = 16; w; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
+        s *= a.scale_log2;
+        const float mn = fmaxf(m, s), base = mn == -INFINITY ? 0.f : mn;
+        const float f = exp2f(m - base), p = exp2f(s - base);
+        m = mn;
+        l = l * f + p;
+        o.x = fmaf(p, v.x, o.x * f), o.y = fmaf(p, v.y, o.y * f), o.z = fmaf(p, v.z, o.z * f), o.w = fmaf(p, v.w, o.w * f);
+    }
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+    return l == 0.f ? -INFINITY : m + log2f(l);
+}
+
+// rows of a tile of the few-rows kernel
+inline int rows_tile(int G, int64_t Tq, int B) { return Tq * G <= 8 * (B < Tq ? B : Tq) ? 8 : 16; }
+
+// Shared memory size (and clusters of 16 blocks) of a kernel, set once per device.
+inline vdm_status prepare_kernel(std::atomic<uint64_t>& ready, const void* f, int smem, bool clusters = false) {
+    int dev = 0;
+    VDM_CUDA_TRY(cudaGetDevice(&dev));
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (ready.load() & bit) return VDM_OK;
+    VDM_CUDA_TRY(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    if (clusters) VDM_CUDA_TRY(cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+    ready.fetch_or(bit);
+    return VDM_OK;
+}
+
 // launchers
+vdm_status launch_attention_rows(const AttnArgs& a, cudaStream_t s);
 vdm_status launch_attention_simt(const AttnArgs& a, vdm_dtype dt, cudaStream_t s);
 vdm_status launch_attention_tc(const AttnArgs& a, cudaStream_t s);
 vdm_status launch_combine(const AttnArgs& a, vdm_dtype dt, cudaStream_t s);
