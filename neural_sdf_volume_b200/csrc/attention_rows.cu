@@ -8,11 +8,12 @@
 // of KS keys.  Each warp keeps a ring of steps in shared memory of its own, filled by 16-byte
 // asynchronous copies (no barrier between warps until the end), and runs the softmax's running
 // maximum and sum on its keys alone:
-//   S = Q K^T    mma.sync m16n8k16, rows of the tile as M, keys as N.  A contraction's order is
-//                free, so lane t of a key's four takes 16 contiguous bytes of it and Q is laid out
-//                to match: K goes from shared memory into fragments without a transposition.
-//   O += P V     P's fragments are S's accumulators; lane g takes 16 contiguous bytes (as columns
-//                of O) of the four rows it needs, paired by byte permutations.
+//   S^T = K Q^T    mma.sync m16n8k16, 16 keys as M and 8 rows of the tile as N.  A contraction's
+//                  order is free, so lane t of a key's four takes 16 contiguous bytes of it and Q is
+//                  laid out to match: K goes from shared memory into fragments without a transposition.
+//   O^T += V^T P^T the weights' 8 x 8 blocks are transposed in registers (movmatrix); lane g takes 16
+//                  contiguous bytes (dimensions, as M) of the four keys it needs, paired by byte
+//                  permutations.
 // mma.sync, not tcgen05: with 1 to 16 rows the tensor work is 1/8 of a tile's and hidden behind the
 // loads, and operands in registers skip the staging that widening 8-bit codes in shared memory
 // would take.
@@ -48,7 +49,7 @@ template <int D, int SRC> struct Cfg {
     static constexpr int RB = E8 ? D : 2 * D;               // bytes of a row
     static constexpr int KS = RB > 128 ? 16 : 32;           // keys of a step
     static constexpr int STAGE = 2 * KS * RB + (E8 ? 2 * KS : 0);
-    static constexpr int NS = RB > 64 ? 3 : 4;              // steps in a warp's ring
+    static constexpr int NS = RB > 64 ? 2 : 4;              // steps in a warp's ring
     static constexpr int PART = RM * D * 4;                 // a warp's O, in its ring at the end
     static constexpr int WARP = NS * STAGE > PART ? NS * STAGE : PART;
     static constexpr int SMEM = RW * WARP;
@@ -62,10 +63,13 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
     return v;
 }
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-    return v;
+template <int W>
+__device__ __forceinline__ void lds128(uint32_t a, uint32_t (&v)[W]) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2 % W]), "=r"(v[3 % W]) : "r"(a));
+}
+template <int W>
+__device__ __forceinline__ void lds64(uint32_t a, uint32_t (&v)[W]) {
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(a));
 }
 __device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
     uint32_t v;
@@ -95,27 +99,63 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// an 8 x 8 block of 16-bit elements transposed across the warp
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
 
-// two e4m3 codes (low or high half of w) as fp16
-template <bool HI>
-__device__ __forceinline__ uint32_t widen(uint32_t w) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(HI ? w >> 16 : w & 0xffffu), __NV_E4M3);
-    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+// four e4m3 codes as two pairs of fp16
+__device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Where chunk c of row r lies in a step's rows.  Keys: the eight lanes of a quarter of a 16-byte load
+// read four neighbouring chunks of two rows; values: two chunks of the rows 0, 2, 4, 6.
+template <int CH>
+__device__ __forceinline__ int swizzle_k(int r, int c) { return CH > 4 ? c ^ ((r & 1) << 2) : c; }
+template <int CH>
+__device__ __forceinline__ int swizzle_v(int r, int c) { return CH > 4 ? c ^ (((r >> 1) & 3) << 1) : c ^ (((r >> 1) & 1) << 1); }
+
+// A row's parts of the block's warps as one: maximum (result), sum and elements.
+template <int WARP>
+__device__ __forceinline__ float join_warps(const float (&sm)[RW][RM], const float (&sl)[RW][RM], uint32_t at, int row, bool on, float& L, float4& x) {
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < RW; ++w) M = fmaxf(M, sm[w][row]);
+    const float ref = M == -INFINITY ? 0.f : M;
+    L = 0.f;
+    x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < RW; ++w) {
+        const float pm = sm[w][row], pl = sl[w][row];
+        const float f = pm == -INFINITY && pl == 0.f ? 0.f : exp2f(pm - ref);
+        L = fmaf(f, pl, L);
+        if (on) {
+            const uint4 y = lds128(at + w * WARP);
+            x.x = fmaf(f, __uint_as_float(y.x), x.x), x.y = fmaf(f, __uint_as_float(y.y), x.y);
+            x.z = fmaf(f, __uint_as_float(y.z), x.z), x.w = fmaf(f, __uint_as_float(y.w), x.w);
+        }
+    }
+    return M;
+}
+
 // ROWS8: tiles have at most 8 rows, the other half of the matrix product's rows stays empty
 template <int D, int SRC, bool ROWS8>
-__global__ void __launch_bounds__(RW * 32) attention_rows_kernel(const __grid_constant__ AttnArgs a, const int cluster) {
+__global__ void __launch_bounds__(RW * 32, 3) attention_rows_kernel(const __grid_constant__ AttnArgs a, const int cluster) {
     using C = Cfg<D, SRC>;
     constexpr bool E8 = C::E8, PAGED = SRC != kPacked;
     constexpr int RB = C::RB, KS = C::KS, NS = C::NS, CH = RB / 16;   // CH: 16-byte chunks of a row
-    constexpr int NR = ROWS8 ? 1 : 2;                                 // rows of a lane: g and g + 8
+    constexpr int NQ = ROWS8 ? 1 : 2;                                 // tiles of 8 rows
     constexpr int EC = E8 ? 16 : 8;                                   // elements of a chunk
-    constexpr int KK = D / 16, NT = D / 8;
+    constexpr int KK = D / 16;
     extern __shared__ __align__(128) uint8_t dyn[];
     __shared__ float s_m[RW][RM], s_l[RW][RM];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
@@ -147,28 +187,32 @@ __global__ void __launch_bounds__(RW * 32) attention_rows_kernel(const __grid_co
             for (int u = 0; u < U; ++u) {
                 const int pos0 = step * KS + 16 * u;
                 const char *sk, *sv;
-                int64_t st, row0 = 0;
+                int64_t row0 = 0;
                 bool on = true;
                 if (PAGED) {
                     on = pg[u] >= 0 && pg[u] < a.c.num_pages;
                     row0 = on ? (((int64_t)pg[u] * a.c.H + hk) << a.c.page_shift) + (pos0 & (a.c.page_size - 1)) : 0;
-                    sk = a.c.k + row0 * RB, sv = a.c.v + row0 * RB, st = RB;
+                    sk = a.c.k + row0 * RB, sv = a.c.v + row0 * RB;
                 } else {
                     sk = a.k.p + (t.k0 + pos0) * a.k.st + hk * a.k.sh;
                     sv = a.v.p + (t.k0 + pos0) * a.v.st + hk * a.v.sh;
-                    st = 0;
                 }
+                if (on && pos0 + 16 <= t.nk) {
 #pragma unroll
-                for (int i = 0; i < CH / 2; ++i) {
-                    const int x = lane + 32 * i, r = x / CH, c = x % CH;
-                    const bool ok = on && pos0 + r < t.nk;
-                    const uint32_t pk = CH > 4 ? c ^ ((r & 1) << 2) : c;
-                    const uint32_t pv = CH > 4 ? c ^ (((r >> 1) & 3) << 1) : c ^ (((r >> 1) & 1) << 1);
-                    const int64_t ok_r = ok ? r : 0;   // an address inside the tensors also where nothing is read
-                    const char* ak = PAGED ? sk + ok_r * st : (ok ? sk + r * a.k.st : a.k.p);
-                    const char* av = PAGED ? sv + ok_r * st : (ok ? sv + r * a.v.st : a.v.p);
-                    cp16(dk + (16 * u + r) * RB + pk * 16, ak + (ok ? c * 16 : 0), ok);
-                    cp16(dv + (16 * u + r) * RB + pv * 16, av + (ok ? c * 16 : 0), ok);
+                    for (int i = 0; i < CH / 2; ++i) {
+                        const int x = lane + 32 * i, r = x / CH, c = x % CH;
+                        cp16(dk + (16 * u + r) * RB + swizzle_k<CH>(r, c) * 16, sk + r * (PAGED ? RB : a.k.st) + c * 16, true);
+                        cp16(dv + (16 * u + r) * RB + swizzle_v<CH>(r, c) * 16, sv + r * (PAGED ? RB : a.v.st) + c * 16, true);
+                    }
+                } else {
+                    // no page, or the sequence ends here: zeros (nothing is read, the address stays inside the tensors)
+#pragma unroll
+                    for (int i = 0; i < CH / 2; ++i) {
+                        const int x = lane + 32 * i, r = x / CH, c = x % CH;
+                        const bool ok = on && pos0 + r < t.nk;
+                        cp16(dk + (16 * u + r) * RB + swizzle_k<CH>(r, c) * 16, ok ? sk + r * (PAGED ? RB : a.k.st) + c * 16 : PAGED ? a.c.k : a.k.p, ok);
+                        cp16(dv + (16 * u + r) * RB + swizzle_v<CH>(r, c) * 16, ok ? sv + r * (PAGED ? RB : a.v.st) + c * 16 : PAGED ? a.c.v : a.v.p, ok);
+                    }
                 }
                 if (E8 && lane < 2) cp16(dk + 2 * KS * RB + lane * KS + 16 * u, (lane ? a.c.vs : a.c.ks) + row0, on);
             }
@@ -183,21 +227,19 @@ __global__ void __launch_bounds__(RW * 32) attention_rows_kernel(const __grid_co
     }
     pages_of(first + (NS - 1) * stride, pg);
 
-    // queries as fragments: element pair i of k-step kk of lane t4 is d = 16-byte chunk
-    // (t4 + 4 h) of the row, elements 4 i + {0, 1} and {2, 3}
-    uint32_t qa[KK][NR][2];
-    float rs[NR];       // factor of the row's scores: softmax scale, log2 e and 2^(Q's exponent)
-    int seen[NR];
+    // queries as fragments, row 8 r + g: the pairs of k-step kk of lane t4 are elements
+    // 4 i + {0, 1} and {2, 3} of the row's 16-byte (in the keys' type) chunk t4 + 4 h
+    uint32_t qb[KK][NQ][2];
+    float rs[NQ][2];     // rows 8 r + 2 t4 + j: factor of the scores (softmax scale, log2 e, Q's exponent)
+    int seen[NQ][2];     // and the keys that the row sees
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
+    for (int r = 0; r < NQ; ++r) {
         const int row = g + 8 * r;
         const bool on = row < n_rows;
         const int rr = t.row0 + (on ? row : 0);
-        seen[r] = on ? keys_seen(a, t, rr / a.G) : 0;
         const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q.p + (t.q0 + rr / a.G) * a.q.st +
                                                                         (int64_t)(hk * a.G + rr % a.G) * a.q.sh);
-        float mul = 1.0f;
-        rs[r] = a.scale_log2;
+        float mul = 1.0f, back = a.scale_log2;
         if (E8) {
             float mx = 0.f;
             if (on)
@@ -210,31 +252,34 @@ __global__ void __launch_bounds__(RW * 32) attention_rows_kernel(const __grid_co
             // exponent e of the maximum (2^e <= mx < 2^(e+1)); Q' = Q 2^(14 - e)
             const int e = mx > 0.f ? (int)(__float_as_uint(mx) >> 23) - 127 : 14, up = min(14 - e, 120);
             mul = pow2i(up);
-            rs[r] = a.scale_log2 * pow2i(-up);
+            back *= pow2i(-up);
         }
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
             const int h = kk / (EC / 4), i = kk % (EC / 4), d = (t4 + 4 * h) * EC + 4 * i;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             if (on) x = load4f(q + d);
-            if (E8) {
-                qa[kk][r][0] = pack_f16(x.x * mul, x.y * mul);
-                qa[kk][r][1] = pack_f16(x.z * mul, x.w * mul);
-            } else {
-                qa[kk][r][0] = pack_bf16(x.x, x.y);
-                qa[kk][r][1] = pack_bf16(x.z, x.w);
-            }
+            qb[kk][r][0] = E8 ? pack_f16(x.x * mul, x.y * mul) : pack_bf16(x.x, x.y);
+            qb[kk][r][1] = E8 ? pack_f16(x.z * mul, x.w * mul) : pack_bf16(x.z, x.w);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int qr = 8 * r + 2 * t4 + j;
+            rs[r][j] = __shfl_sync(0xffffffffu, back, 4 * (2 * t4 + j));
+            seen[r][j] = qr < n_rows ? keys_seen(a, t, (t.row0 + qr) / a.G) : 0;
         }
     }
+    const int all_see = keys_seen(a, t, t.row0 / a.G);   // keys that every row of the tile sees
 
-    float o[NT][4];
+    float o[KK][NQ][4];
+    float m[NQ][2], l[NQ][2];
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int r = 0; r < NQ; ++r) {
+        m[r][0] = m[r][1] = -INFINITY;
+        l[r][0] = l[r][1] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-    float m[NR], l[NR];
-#pragma unroll
-    for (int r = 0; r < NR; ++r) m[r] = -INFINITY, l[r] = 0.f;
+        for (int i = 0; i < KK; ++i) o[i][r][0] = o[i][r][1] = o[i][r][2] = o[i][r][3] = 0.f;
+    }
     constexpr float W0 = E8 ? 12.0f : 0.0f;   // fp16 weights are kept at 2^12 times their value
 
     int slot = 0, fill = NS - 1;
@@ -247,120 +292,141 @@ __global__ void __launch_bounds__(RW * 32) attention_rows_kernel(const __grid_co
         const uint32_t bk = ring + slot * C::STAGE, bv = bk + KS * RB;
         slot = slot + 1 == NS ? 0 : slot + 1;
 
-        float s[KS / 8][4];
+        // scores: s[u][r][2 half + j] is key 16 u + 8 half + g, row 8 r + 2 t4 + j
+        float s[U][NQ][4];
 #pragma unroll
-        for (int n = 0; n < KS / 8; ++n) {
-            s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-            const int r = 8 * n + g;
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int r = 0; r < NQ; ++r) s[u][r][0] = s[u][r][1] = s[u][r][2] = s[u][r][3] = 0.f;
+            const uint32_t row = bk + (16 * u + g) * RB;
 #pragma unroll
             for (int h = 0; h < CH / 4; ++h) {
-                const int c = t4 + 4 * h;
-                const uint4 w = lds128(bk + r * RB + (CH > 4 ? c ^ ((r & 1) << 2) : c) * 16);
-                const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                const uint32_t at = swizzle_k<CH>(g, t4 + 4 * h) * 16;
+                const uint4 w0 = lds128(row + at), w1 = lds128(row + 8 * RB + at);
+                const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
                 for (int i = 0; i < EC / 4; ++i) {
-                    const int kk = h * (EC / 4) + i;
-                    const uint32_t b0 = E8 ? widen<false>(x[i]) : x[2 * i % 4], b1 = E8 ? widen<true>(x[i]) : x[(2 * i + 1) % 4];
-                    mma16816<E8>(s[n], qa[kk][0][0], ROWS8 ? 0u : qa[kk][NR - 1][0], qa[kk][0][1], ROWS8 ? 0u : qa[kk][NR - 1][1], b0, b1);
+                    uint32_t a0, a1, a2, a3;
+                    if (E8) widen(x0[i], a0, a2), widen(x1[i], a1, a3);
+                    else a0 = x0[2 * i % 4], a1 = x1[2 * i % 4], a2 = x0[(2 * i + 1) % 4], a3 = x1[(2 * i + 1) % 4];
+#pragma unroll
+                    for (int r = 0; r < NQ; ++r)
+                        mma16816<E8>(s[u][r], a0, a1, a2, a3, qb[h * (EC / 4) + i][r][0], qb[h * (EC / 4) + i][r][1]);
                 }
             }
         }
-        // scores in log2 units, with the value scale's exponent added
-        float inv[KS / 8][2];   // 2^-e of the keys
-        float mx[NR];
+        // in log2 units, with the value scale's exponent added; inv: 2^-exponent
+        float inv[U][2];
+        if (E8) {
+            static_assert(!E8 || KS == 32, "a lane per key");
+            const uint32_t kb = lds_u8(bk + 2 * KS * RB + lane), vb = lds_u8(bk + 2 * KS * RB + KS + lane);
+            const float f_ = scale_of((uint8_t)kb);
+            const float ev_ = __uint_as_float(0x4b000000u | vb) - (8388608.0f + 127.0f);   // 2^23 + vb as a float
+            const float inv_ = __uint_as_float((uint32_t)max(1, 254 - (int)vb) << 23);     // beyond 253 not from vdm_cache_write
 #pragma unroll
-        for (int r = 0; r < NR; ++r) mx[r] = -INFINITY;
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int n = 0; n < KS / 8; ++n)
+                for (int k = 0; k < 2; ++k) {
+                    const int src = 16 * u + 8 * k + g;
+                    const float f = __shfl_sync(0xffffffffu, f_, src), ev = __shfl_sync(0xffffffffu, ev_, src);
+                    inv[u][k] = __shfl_sync(0xffffffffu, inv_, src);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int key = 8 * n + 2 * t4 + j;
-                float f = 1.0f, ev = 0.0f;
-                if (E8) {
-                    f = scale_of((uint8_t)lds_u8(bk + 2 * KS * RB + key));
-                    const int vb = (int)lds_u8(bk + 2 * KS * RB + KS + key);
-                    ev = (float)(vb - 127);
-                    // 2^(127 - vb); vb up to 246 from vdm_cache_write, beyond 253 the sum loses denormals
-                    inv[n][j] = __uint_as_float((uint32_t)max(1, 254 - vb) << 23);
+                    for (int r = 0; r < NQ; ++r)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) s[u][r][2 * k + j] = fmaf(s[u][r][2 * k + j], rs[r][j] * f, ev);
                 }
+        } else {
 #pragma unroll
-                for (int r = 0; r < NR; ++r) {
-                    float& x = s[n][2 * r + j];
-                    x = E8 ? fmaf(x, rs[r] * f, ev) : x * rs[r];
-                    if (step * KS + key >= seen[r]) x = -INFINITY;
-                    mx[r] = fmaxf(mx[r], x);
-                }
-            }
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int r = 0; r < NQ; ++r)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[u][r][e] *= rs[r][e & 1];
+        }
+        if ((step + 1) * KS > all_see) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int r = 0; r < NQ; ++r)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (step * KS + 16 * u + 8 * (e >> 1) + g >= seen[r][e & 1]) s[u][r][e] = -INFINITY;
+        }
+        float mx[NQ][2];
         bool raise = false;
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-            raise = raise || mx[r] > m[r] + 3.0f;
-        }
+        for (int r = 0; r < NQ; ++r)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float x = fmaxf(s[0][r][j], s[0][r][2 + j]);
+#pragma unroll
+                for (int u = 1; u < U; ++u) x = fmax3(x, s[u][r][j], s[u][r][2 + j]);
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                mx[r][j] = x;
+                raise = raise || x > m[r][j] + 3.0f;
+            }
         if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                const float mn = fmaxf(m[r], mx[r]);
-                const float f = mn == -INFINITY ? 1.0f : exp2f(m[r] - mn);
-                m[r] = mn;
-                l[r] *= f;
+            for (int r = 0; r < NQ; ++r)
 #pragma unroll
-                for (int i = 0; i < NT; ++i) o[i][2 * r] *= f, o[i][2 * r + 1] *= f;
-            }
-        }
-        uint32_t p[KS / 8][NR];
+                for (int j = 0; j < 2; ++j) {
+                    const float mn = fmaxf(m[r][j], mx[r][j]);
+                    const float f = mn == -INFINITY ? 1.0f : exp2f(m[r][j] - mn);
+                    m[r][j] = mn;
+                    l[r][j] *= f;
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            const float ref = (m[r] == -INFINITY ? 0.f : m[r]) - W0;
-#pragma unroll
-            for (int n = 0; n < KS / 8; ++n) {
-                const float w0 = ex2(s[n][2 * r] - ref), w1 = ex2(s[n][2 * r + 1] - ref);
-                if (E8) l[r] = fmaf(w0, inv[n][0], fmaf(w1, inv[n][1], l[r]));
-                else l[r] += w0 + w1;
-                p[n][r] = E8 ? pack_f16(w0, w1) : pack_bf16(w0, w1);
-            }
-        }
-#pragma unroll
-        for (int kg = 0; kg < KS / 16; ++kg) {
-            const uint32_t a0 = p[2 * kg][0], a1 = ROWS8 ? 0u : p[2 * kg][NR - 1], a2 = p[2 * kg + 1][0], a3 = ROWS8 ? 0u : p[2 * kg + 1][NR - 1];
-            const uint32_t rows = bv + (16 * kg + 2 * t4) * RB;   // this lane's rows: +0, +1, +8, +9
-            if (E8 && D == 64) {
-                // 8 bytes of each row: half of chunk g / 2
-                const uint32_t off = (uint32_t)(((g >> 1) ^ ((t4 & 1) << 1)) * 16 + (g & 1) * 8);
-                const uint2 x0 = lds64(rows + off), x1 = lds64(rows + RB + off), y0 = lds64(rows + 8 * RB + off), y1 = lds64(rows + 9 * RB + off);
-                const uint32_t X0[2] = {x0.x, x0.y}, X1[2] = {x1.x, x1.y}, Y0[2] = {y0.x, y0.y}, Y1[2] = {y1.x, y1.y};
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t u0 = __byte_perm(X0[i], X1[i], 0x5140), u1 = __byte_perm(X0[i], X1[i], 0x7362);
-                    const uint32_t v0 = __byte_perm(Y0[i], Y1[i], 0x5140), v1 = __byte_perm(Y0[i], Y1[i], 0x7362);
-                    mma16816<E8>(o[(4 * i) % NT], a0, a1, a2, a3, widen<false>(u0), widen<false>(v0));
-                    mma16816<E8>(o[(4 * i + 1) % NT], a0, a1, a2, a3, widen<true>(u0), widen<true>(v0));
-                    mma16816<E8>(o[(4 * i + 2) % NT], a0, a1, a2, a3, widen<false>(u1), widen<false>(v1));
-                    mma16816<E8>(o[(4 * i + 3) % NT], a0, a1, a2, a3, widen<true>(u1), widen<true>(v1));
+                    for (int i = 0; i < KK; ++i) o[i][r][j] *= f, o[i][r][2 + j] *= f;
                 }
-            } else {
+        }
+        uint32_t p[U][NQ][2];   // weights of keys 16 u + 8 half + 2 t4 + {0, 1}, row 8 r + g
 #pragma unroll
-                for (int h = 0; h < CH / 8; ++h) {
-                    const uint32_t off = (uint32_t)((g ^ (t4 << 1)) + 8 * h) * 16;   // rows 2 t4 + {0, 1, 8, 9}: (r / 2) % 4 = t4
-                    const uint4 x0 = lds128(rows + off), x1 = lds128(rows + RB + off), y0 = lds128(rows + 8 * RB + off),
-                                y1 = lds128(rows + 9 * RB + off);
-                    const uint32_t X0[4] = {x0.x, x0.y, x0.z, x0.w}, X1[4] = {x1.x, x1.y, x1.z, x1.w}, Y0[4] = {y0.x, y0.y, y0.z, y0.w},
-                                   Y1[4] = {y1.x, y1.y, y1.z, y1.w};
+        for (int r = 0; r < NQ; ++r) {
+            const float ref0 = (m[r][0] == -INFINITY ? 0.f : m[r][0]) - W0, ref1 = (m[r][1] == -INFINITY ? 0.f : m[r][1]) - W0;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (E8) {
-                            const uint32_t u0 = __byte_perm(X0[i], X1[i], 0x5140), u1 = __byte_perm(X0[i], X1[i], 0x7362);
-                            const uint32_t v0 = __byte_perm(Y0[i], Y1[i], 0x5140), v1 = __byte_perm(Y0[i], Y1[i], 0x7362);
-                            mma16816<E8>(o[(4 * i) % NT], a0, a1, a2, a3, widen<false>(u0), widen<false>(v0));
-                            mma16816<E8>(o[(4 * i + 1) % NT], a0, a1, a2, a3, widen<true>(u0), widen<true>(v0));
-                            mma16816<E8>(o[(4 * i + 2) % NT], a0, a1, a2, a3, widen<false>(u1), widen<false>(v1));
-                            mma16816<E8>(o[(4 * i + 3) % NT], a0, a1, a2, a3, widen<true>(u1), widen<true>(v1));
-                        } else {
-                            const int n = 8 * h + 2 * i;
-                            mma16816<E8>(o[n % NT], a0, a1, a2, a3, __byte_perm(X0[i], X1[i], 0x5410), __byte_perm(Y0[i], Y1[i], 0x5410));
-                            mma16816<E8>(o[(n + 1) % NT], a0, a1, a2, a3, __byte_perm(X0[i], X1[i], 0x7632), __byte_perm(Y0[i], Y1[i], 0x7632));
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float w0 = ex2(s[u][r][2 * k] - ref0), w1 = ex2(s[u][r][2 * k + 1] - ref1);
+                    l[r][0] = E8 ? fmaf(w0, inv[u][k], l[r][0]) : l[r][0] + w0;
+                    l[r][1] = E8 ? fmaf(w1, inv[u][k], l[r][1]) : l[r][1] + w1;
+                    p[u][r][k] = transpose8(E8 ? pack_f16(w0, w1) : pack_bf16(w0, w1));
+                }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t rows = bv + (16 * u + 2 * t4) * RB;   // this lane's keys: +0, +1, +8, +9
+            constexpr int W = E8 && D == 64 ? 2 : 4;             // words of a key that a lane reads at once
+#pragma unroll
+            for (int h = 0; h < KK * 2 / (W * (E8 ? 4 : 2)); ++h) {
+                uint32_t x0[W], x1[W], y0[W], y1[W];
+                if constexpr (W == 2) {
+                    const uint32_t off = (uint32_t)(swizzle_v<CH>(2 * t4, g >> 1) * 16 + (g & 1) * 8);
+                    lds64(rows + off, x0), lds64(rows + RB + off, x1), lds64(rows + 8 * RB + off, y0), lds64(rows + 9 * RB + off, y1);
+                } else {
+                    const uint32_t off = (uint32_t)swizzle_v<CH>(2 * t4, g + 8 * h) * 16;
+                    lds128(rows + off, x0), lds128(rows + RB + off, x1), lds128(rows + 8 * RB + off, y0), lds128(rows + 9 * RB + off, y1);
+                }
+#pragma unroll
+                for (int i = 0; i < W; ++i) {
+                    if (E8) {
+                        // elements 4 i .. 4 i + 3, each as a pair of keys
+                        uint32_t e0, e1, e2, e3, f0, f1, f2, f3;
+                        widen(__byte_perm(x0[i], x1[i], 0x5140), e0, e1);
+                        widen(__byte_perm(x0[i], x1[i], 0x7362), e2, e3);
+                        widen(__byte_perm(y0[i], y1[i], 0x5140), f0, f1);
+                        widen(__byte_perm(y0[i], y1[i], 0x7362), f2, f3);
+#pragma unroll
+                        for (int r = 0; r < NQ; ++r) {
+                            mma16816<E8>(o[(2 * i) % KK][r], e0, e1, f0, f1, p[u][r][0], p[u][r][1]);
+                            mma16816<E8>(o[(2 * i + 1) % KK][r], e2, e3, f2, f3, p[u][r][0], p[u][r][1]);
                         }
+                    } else {
+                        const uint32_t e0 = __byte_perm(x0[i], x1[i], 0x5410), e1 = __byte_perm(x0[i], x1[i], 0x7632);
+                        const uint32_t f0 = __byte_perm(y0[i], y1[i], 0x5410), f1 = __byte_perm(y0[i], y1[i], 0x7632);
+#pragma unroll
+                        for (int r = 0; r < NQ; ++r) mma16816<E8>(o[(4 * h + i) % KK][r], e0, e1, f0, f1, p[u][r][0], p[u][r][1]);
                     }
                 }
             }
@@ -370,48 +436,70 @@ __global__ void __launch_bounds__(RW * 32) attention_rows_kernel(const __grid_co
     cp_async_wait<0>();
     __syncwarp();
 
-    // the warp's rows into its ring, column n-tile i, lane column j: element of the row
-    const float w0 = exp2f(-W0);
+    // the warp's rows into its ring
+    const float w0 = pow2i(-(int)W0);
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-        l[r] *= w0;
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-        if (t4 == 0) s_m[warp][g + 8 * r] = m[r], s_l[warp][g + 8 * r] = l[r];
-    }
+    for (int r = 0; r < NQ; ++r)
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+        for (int j = 0; j < 2; ++j) {
+            const int row = 8 * r + 2 * t4 + j;
+            float x = l[r][j] * w0;
+            x += __shfl_xor_sync(0xffffffffu, x, 4);
+            x += __shfl_xor_sync(0xffffffffu, x, 8);
+            x += __shfl_xor_sync(0xffffffffu, x, 16);
+            if (g == 0) s_m[warp][row] = m[r][j], s_l[warp][row] = x;
 #pragma unroll
-        for (int e = 0; e < 2 * NR; ++e) {
-            // column j = 2 t4 + (e & 1) of n-tile i: the dimensions that lane group g = j loaded as i
-            const int row = g + 8 * (e >> 1), j = 2 * t4 + (e & 1);
-            const int d = E8 ? j * (D / 8) + i : (i / 8) * 64 + j * 8 + i % 8;
-            const float x = o[i][e] * w0;
-            asm volatile("st.shared.f32 [%0], %1;" ::"r"(ring + (row * D + d) * 4), "f"(x) : "memory");
+            for (int i = 0; i < KK; ++i) {
+                // elements 2 i and 2 i + 1 of the ones that this lane's group loaded of each key
+                const int d = E8 ? g * (D / 8) + 2 * i : (2 * i / 8) * 64 + g * 8 + 2 * i % 8;
+                asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(ring + (row * D + d) * 4), "f"(o[i][r][j] * w0), "f"(o[i][r][2 + j] * w0) : "memory");
+            }
         }
-    if (cluster > 1) cluster_sync();
-    else __syncthreads();
+    __syncthreads();
 
-    // joining: a warp of the cluster per row, parts in order
+    // joining: a row's parts in order, first the block's warps, then the cluster's blocks
+    const bool on = 4 * lane < D;
+    const uint32_t part = smem_u32(dyn);
+    if (cluster > 1) {
+        for (int row = warp; row < n_rows; row += RW) {
+            float L;
+            float4 x;
+            const float M = join_warps<C::WARP>(s_m, s_l, part + (row * D + 4 * lane) * 4, row, on, L, x);
+            __syncwarp();
+            if (on)
+                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(part + (row * D + 4 * lane) * 4), "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w) : "memory");
+            if (lane == 0) s_m[0][row] = M, s_l[0][row] = L;
+        }
+        cluster_sync();
+    }
     for (int row = rank * RW + warp; row < n_rows; row += cluster * RW) {
-        float M = -INFINITY;
-        for (int k = 0; k < cluster; ++k)
-            for (int w = 0; w < RW; ++w) M = fmaxf(M, ld_cluster_f32(mapa(smem_u32(&s_m[w][row]), k)));
-        const float ref = M == -INFINITY ? 0.f : M;
-        float L = 0.f;
+        float L = 0.f, ref;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        const bool on = 4 * lane < D;
-        for (int k = 0; k < cluster; ++k)
-            for (int w = 0; w < RW; ++w) {
-                const float pm = ld_cluster_f32(mapa(smem_u32(&s_m[w][row]), k)), pl = ld_cluster_f32(mapa(smem_u32(&s_l[w][row]), k));
-                if (pm == -INFINITY && pl == 0.f) continue;   // no key
-                const float f = exp2f(pm - ref);
-                L = fmaf(f, pl, L);
+        if (cluster == 1) {
+            const float M = join_warps<C::WARP>(s_m, s_l, part + (row * D + 4 * lane) * 4, row, on, L, x);
+            ref = M == -INFINITY ? 0.f : M;
+        } else {
+            // lane k: block k's maximum and sum
+            float pm = -INFINITY, pl = 0.f;
+            if (lane < cluster) {
+                pm = ld_cluster_f32(mapa(smem_u32(&s_m[0][row]), lane));
+                pl = ld_cluster_f32(mapa(smem_u32(&s_l[0][row]), lane));
+            }
+            float M = pm;
+#pragma unroll
+            for (int w = 16; w; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+            ref = M == -INFINITY ? 0.f : M;
+            const float pf = pm == -INFINITY && pl == 0.f ? 0.f : exp2f(pm - ref);   // no key: nothing
+#pragma unroll 4
+            for (int k = 0; k < cluster; ++k) {
+                const float f = __shfl_sync(0xffffffffu, pf, k);
+                L = fmaf(f, __shfl_sync(0xffffffffu, pl, k), L);
                 if (on) {
-                    const float4 y = ld_cluster_f4(mapa(smem_u32(dyn) + w * C::WARP + (row * D + 4 * lane) * 4, k));
+                    const float4 y = ld_cluster_f4(mapa(part + (row * D + 4 * lane) * 4, k));
                     x.x = fmaf(f, y.x, x.x), x.y = fmaf(f, y.y, x.y), x.z = fmaf(f, y.z, x.z), x.w = fmaf(f, y.w, x.w);
                 }
             }
+        }
         const float inv = L == 0.f ? 0.f : 1.0f / L;
         x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
         float lse2 = L == 0.f ? -INFINITY : ref + log2f(L);

@@ -127,7 +127,7 @@ Plan plan_attention(const vdm_attention* at, int B, int64_t Tq, int64_t max_kv) 
         p.kernel = kRows;
         const int64_t M = rows_tile((int)G, Tq, B), tiles = (Tq * G + seqs * (M - 1)) / M * at->Hk;
         const int64_t steps = (max_kv + 31) / 32;
-        while (p.cluster < 16 && tiles * p.cluster < 2400 && p.cluster * 8 < steps) p.cluster *= 2;
+        while (p.cluster < 16 && tiles * p.cluster < 1500 && p.cluster * 4 <= steps) p.cluster *= 2;
         if (p.cluster == 16)
             while (p.splits < 16 && tiles * p.cluster * p.splits < 296 && p.splits * p.cluster * 32 < steps) p.splits *= 2;
         return p;

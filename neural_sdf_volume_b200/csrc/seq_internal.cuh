@@ -69,11 +69,21 @@ __device__ __forceinline__ int cache_len(const CacheView& c, int32_t len) {
 __device__ __forceinline__ bool find_tile(const AttnArgs& a, int64_t idx, int M, bool last_first, RowTile& t) {
     const int lane = threadIdx.x & 31;
     int64_t done = 0;
+    int32_t lo[4], hi[4];   // offsets of the next 128 sequences, asked for together
     for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const int b = b0 + lane;
+        const int b = b0 + lane, part = (b0 >> 5) & 3;
+        if (part == 0) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                if (b + 32 * p < a.B) lo[p] = a.cu_q[b + 32 * p], hi[p] = a.cu_q[b + 32 * p + 1];
+        }
         int64_t start = 0;
         int n = 0;
-        if (b < a.B) n = clamp_len(a.cu_q[b], a.cu_q[b + 1], a.Tq, &start);
+        if (b < a.B) {
+            const int32_t l = part == 0 ? lo[0] : part == 1 ? lo[1] : part == 2 ? lo[2] : lo[3];
+            const int32_t h = part == 0 ? hi[0] : part == 1 ? hi[1] : part == 2 ? hi[2] : hi[3];
+            n = clamp_len(l, h, a.Tq, &start);
+        }
         const int64_t tiles = ((int64_t)n * a.G + M - 1) / M;
         int64_t incl = tiles;
 #pragma unroll
