@@ -44,6 +44,12 @@ namespace {
 using namespace ptx;
 
 constexpr int BM = 128, BN = 128;
+#ifndef VDM_POLY64
+#define VDM_POLY64 3
+#define VDM_POLY128 2
+#endif
+constexpr int THREADS = 384;                        // three warpgroups, launched with 168 registers a thread
+constexpr int REGS_SOFTMAX = 208, REGS_OTHER = 88;  // 2 * 208 + 88 = 3 * 168
 enum Source : int { kPacked = 0, kPagedBf16 = 1, kPagedE4m3 = 2 };
 constexpr uint32_t T_O = 256;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -127,7 +133,7 @@ __device__ __forceinline__ void st_v4(uint32_t addr, uint32_t a, uint32_t b, uin
 }
 
 template <int D, int SRC>
-__global__ void __launch_bounds__(SRC == kPagedE4m3 ? 384 : 320, 1)
+__global__ void __launch_bounds__(THREADS, 1)
 attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __grid_constant__ AttnArgs a, const int tok_first) {
     using C = Cfg<D>;
@@ -196,6 +202,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 
     if (warp < 8) {
         // ------------------------------------------------------------ softmax
+        regs_up<REGS_SOFTMAX>();
         const int w = warp >> 2;
         const int row = t.row0 + w * BM + (tid & 127);
         const int seen = row < total_rows ? keys_seen(a, t, row / a.G) : 0;
@@ -224,11 +231,14 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             float mx[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                mx[c] = fmaxf(s[c][0], s[c][1]);
+                mx[c] = fmax3_nan(s[c][0], s[c][1], s[c][2]);
 #pragma unroll
-                for (int i = 2; i < 32; i += 2) mx[c] = fmax3(mx[c], s[c][i], s[c][i + 1]);
+                for (int i = 3; i < 31; i += 2) mx[c] = fmax3_nan(mx[c], s[c][i], s[c][i + 1]);
             }
-            const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+            const float mt = fmax3_nan(fmax3_nan(mx[0], mx[1], mx[2]), mx[3], fmax3_nan(s[0][31], s[1][31], fmax3_nan(s[2][31], s[3][31], s[3][31])));
+            // a score that is NaN or +inf: the row's result is NaN, whatever becomes of its weights
+            if (!(mt < INFINITY)) l = __uint_as_float(0x7fc00000u);
+            const float mn = fmaxf(m, mt);
             // raise the reference only when it has grown by more than 2^8 (or was -inf)
             const bool raise = (mn - m) * sc > 8.0f;
             if (__any_sync(0xffffffffu, raise)) {
@@ -255,19 +265,35 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             const float ref = m == -INFINITY ? 0.f : m * sc;
             const uint64_t sc2 = f32x2(sc, sc), ref2 = f32x2(-ref, -ref);
             uint64_t sum = f32x2(0.f, 0.f);
+            // Of every 8 pairs POLY are computed on the FMA pipe: the special-function unit alone takes as
+            // long for a tile as the matrix products at D = 128, twice as long at D = 64.  Masked scores, and
+            // rows that have seen none above -inf, need exact zeros: no polynomials there.
+            const bool plain = __any_sync(0xffffffffu, left < BN || m == -INFINITY);
+            auto weights = [&](auto poly) {
+                constexpr int POLY = decltype(poly)::value;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t p[16];
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t p[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float x0, x1;
-                    f32x2_split(fma_f32x2(f32x2(s[c][2 * i], s[c][2 * i + 1]), sc2, ref2), x0, x1);
-                    const float e0 = ex2(x0), e1 = ex2(x1);
-                    sum = add_f32x2(sum, f32x2(e0, e1));
-                    p[i] = pack_bf16(e0, e1);
+                    for (int i = 0; i < 16; ++i) {
+                        const uint64_t x = fma_f32x2(f32x2(s[c][2 * i], s[c][2 * i + 1]), sc2, ref2);
+                        uint64_t e;
+                        if (i % 8 < POLY) e = exp2_pair_poly(x);
+                        else {
+                            float x0, x1;
+                            f32x2_split(x, x0, x1);
+                            e = f32x2(ex2(x0), ex2(x1));
+                        }
+                        sum = add_f32x2(sum, e);
+                        float e0, e1;
+                        f32x2_split(e, e0, e1);
+                        p[i] = pack_bf16(e0, e1);
+                    }
+                    tmem_st16(ts + 16 * c, p);
                 }
-                tmem_st16(ts + 16 * c, p);
-            }
+            };
+            if (plain) weights(std::integral_constant<int, 0>{});
+            else weights(std::integral_constant<int, D == 64 ? VDM_POLY64 : VDM_POLY128>{});
             float s0, s1;
             f32x2_split(sum, s0, s1);
             l += s0 + s1;
@@ -341,7 +367,9 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             }
         }
         tc_fence_before();
-    } else if (warp == 8) {
+    } else {
+      regs_down<REGS_OTHER>();
+      if (warp == 8) {
         // ------------------------------------------------------------ MMA issue
         constexpr uint32_t id_s = idesc_bf16(BM, BN, false), id_o = idesc_bf16(BM, D, true);
         const int n = jmax - jb;
@@ -475,6 +503,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             fence_proxy_async();
             mbar_arrive(smem_u32(&sh.full[slot]));
         }
+      }
     }
 
     // MMAs in flight read shared memory and write TMEM: wait for the last ones before either goes
@@ -532,7 +561,7 @@ vdm_status launch(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& 
     static std::atomic<uint64_t> ready{0};
     VDM_TRY(prepare_kernel(ready, reinterpret_cast<const void*>(kern), Cfg<D>::SMEM));
     const int64_t tiles = (a.Tq * a.G + (a.B < a.Tq ? a.B : a.Tq) * (int64_t)(2 * BM - 1)) / (2 * BM);
-    kern<<<dim3((unsigned)tiles, a.Hk, a.splits), SRC == kPagedE4m3 ? 384 : 320, Cfg<D>::SMEM, s>>>(mk, mv, a, tok_first);
+    kern<<<dim3((unsigned)tiles, a.Hk, a.splits), THREADS, Cfg<D>::SMEM, s>>>(mk, mv, a, tok_first);
     VDM_TRY(check_launch("attention_tc_kernel"));
     return a.splits > 1 ? launch_combine(a, VDM_BF16, s) : VDM_OK;
 }

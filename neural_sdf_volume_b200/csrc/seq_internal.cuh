@@ -66,8 +66,37 @@ __device__ __forceinline__ int cache_len(const CacheView& c, int32_t len) {
 
 // Tile `idx` of the sequences' row tiles of M rows (whole warps, converged); false: no such tile.
 // With `last_first` a sequence's tiles come in descending order (causal: longest first).
+// Large tiles of up to 32 sequences come by the sequences' keys, longest first: a launch then ends
+// with its short blocks.
 __device__ __forceinline__ bool find_tile(const AttnArgs& a, int64_t idx, int M, bool last_first, RowTile& t) {
     const int lane = threadIdx.x & 31;
+    if (M > 16 && a.B > 1 && a.B <= 32) {
+        int64_t q0 = 0, k0 = 0;
+        int n = 0, nk = -1;
+        if (lane < a.B) {
+            n = clamp_len(a.cu_q[lane], a.cu_q[lane + 1], a.Tq, &q0);
+            if (a.paged) nk = cache_len(a.c, a.cu_k[lane]);
+            else nk = clamp_len(a.cu_k[lane], a.cu_k[lane + 1], a.Tk, &k0);
+        }
+        const int64_t tiles = ((int64_t)n * a.G + M - 1) / M;
+        int64_t before = 0;   // tiles of the sequences that come earlier
+        for (int j = 0; j < a.B; ++j) {
+            const int nj = __shfl_sync(0xffffffffu, nk, j);
+            const int64_t tj = __shfl_sync(0xffffffffu, tiles, j);
+            if (nj > nk || (nj == nk && j < lane)) before += tj;
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, before <= idx && idx < before + tiles);
+        if (!hit) return false;
+        const int src = __ffs(hit) - 1;
+        const int64_t cnt = __shfl_sync(0xffffffffu, tiles, src), local = idx - __shfl_sync(0xffffffffu, before, src);
+        t.b = src;
+        t.nq = __shfl_sync(0xffffffffu, n, src);
+        t.nk = __shfl_sync(0xffffffffu, nk, src);
+        t.q0 = __shfl_sync(0xffffffffu, q0, src);
+        t.k0 = __shfl_sync(0xffffffffu, k0, src);
+        t.row0 = (int)((last_first ? cnt - 1 - local : local) * M);
+        return true;
+    }
     int64_t done = 0;
     int32_t lo[4], hi[4];   // offsets of the next 128 sequences, asked for together
     for (int b0 = 0; b0 < a.B; b0 += 32) {

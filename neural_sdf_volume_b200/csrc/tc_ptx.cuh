@@ -367,6 +367,21 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
+// The same, NaN if any input is.
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// Registers of a warpgroup's threads; the shares of a block's warpgroups add up to at most what it was launched with.
+template <int N>
+__device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 // Packed fp32 pairs (sm_100 f32x2 arithmetic): each lane of the pair is rounded exactly
 // as the scalar instruction would round it, so these are bit-identical to two scalar ops.
 __device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
