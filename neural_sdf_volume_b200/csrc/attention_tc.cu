@@ -4,24 +4,27 @@
 //   S = Q K^T (bf16 in, fp32 in TMEM) ; softmax with the running maximum m and sum l ;
 //   O <- O + P V (P bf16 in TMEM, O fp32 in TMEM) ; out = O / l
 //
-// One CTA takes 256 query rows (row = token x group: the query heads of a key head beside one
-// another, so that a group shares its keys' loads) as two tiles of 128, and runs over the keys
-// in tiles of 128.  Roles:
-//   warps 0-3, 4-7  softmax of tile 0 and 1, one row per thread: S from TMEM, maximum,
-//                   2^(scale log2e s - m), P back into the columns of S (bf16), sum in fp32;
-//   warp 8          issues the MMAs of both tiles in turn: while one tile's softmax runs, the
-//                   tensor cores work on the other's;
-//   warp 9          TMA loads of K and V tiles into a ring of slots (packed: one box of 128
-//                   tokens per 64 columns; paged: one box per page);
-//   warps 9-11      (8-bit cache) instead read codes from global memory, widen them to bf16 -
-//                   exact: a code times a power of two - and write the ring's slots.
+// A CTA takes 256 query rows (D = 128) or 128 (D = 64, two CTAs on an SM) of one sequence and key
+// head - a row is a token and a query head of the group, so that a group shares its keys' loads -
+// as tiles of 128, and runs over the keys in tiles of 128.  Roles, with NT row tiles:
+//   warps 0 .. 4 NT - 1  softmax, one row per thread: S from TMEM, maximum, 2^(scale log2e s - m),
+//                        P as bf16 back into TMEM, sum in fp32; before and after the loop the
+//                        tile's queries into shared memory and its rows out;
+//   warp 4 NT            issues the MMAs of the tiles in turn: while one tile's softmax runs, the
+//                        tensor cores work on the other's (D = 64: on the other CTA's);
+//   warp 4 NT + 1        TMA loads of K and V tiles into a ring of slots (packed: one box of 128
+//                        tokens per 64 columns; paged: one box per page);
+//   warps 4 NT + 1 .. 3  (8-bit cache) instead read codes from global memory, widen them to bf16 -
+//                        exact: a code times a power of two - and write the ring's slots.
 // The maximum that the exponents refer to follows the running maximum only when that has
 // grown by more than 8 (log2 units): then O and l are rescaled, which needs the previous
 // product to have finished; otherwise P stays below 2^8 and nothing is lost.  l sums the fp32
 // exponentials; only the product uses their bf16 roundings.
 //
-// TMEM (512 columns): S0 [0,128) S1 [128,256) O0 [256,256+D) O1 [384,384+D); P_w overwrites
-// the first 64 columns of S_w.
+// TMEM, D = 128 (512 columns): S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512); P_w overwrites the
+// first 64 columns of S_w, so that a tile's next scores come after its product P V.
+// D = 64 (256 columns): S [0,128) P [128,192) O [192,256), and the next scores are computed while the
+// softmax of these runs.
 //
 // Masked keys: a key that a row does not see has weight 0.  V rows behind the sequence's end
 // are zeroed in shared memory (0 * NaN would reach every row); V rows inside the sequence that
@@ -45,31 +48,38 @@ using namespace ptx;
 
 constexpr int BM = 128, BN = 128;
 #ifndef VDM_POLY64
-#define VDM_POLY64 3
-#define VDM_POLY128 2
+#define VDM_POLY64 1
+#define VDM_POLY128 1
 #endif
-constexpr int THREADS = 384;                        // three warpgroups, launched with 168 registers a thread
-constexpr int REGS_SOFTMAX = 208, REGS_OTHER = 88;  // 2 * 208 + 88 = 3 * 168
 enum Source : int { kPacked = 0, kPagedBf16 = 1, kPagedE4m3 = 2 };
-constexpr uint32_t T_O = 256;
 constexpr float kLn2 = 0.69314718055994530942f;
 
 template <int D> struct Cfg {
     static constexpr int PANELS = D / 64;
+    static constexpr int NT = tc_rows(D) / BM;       // row tiles of a CTA
+    static constexpr int PER_SM = NT == 1 ? 2 : 1;
+    static constexpr int THREADS = 128 * NT + 128;
+    // registers a thread, out of 128 (two CTAs of 256 threads) or 168 (one of 384) at launch
+    static constexpr int REGS_SOFTMAX = NT == 1 ? 192 : 208, REGS_OTHER = NT == 1 ? 64 : 88;
     static constexpr int QBYTES = BM * D * 2;        // one query tile
     static constexpr int SLOT = BN * D * 2;          // one key or value tile
-    static constexpr int NS = D == 128 ? 5 : 8;      // slots beside two query tiles in 227 KB
-    static constexpr int SMEM = 2 * QBYTES + NS * SLOT + 1024;
+    static constexpr int NS = D == 128 ? 5 : 6;      // slots beside the query tiles in 227 KB (113 KB)
+    static constexpr int TILES = NT * QBYTES + NS * SLOT;
+    static constexpr bool APART = NT == 1;           // P has columns of its own
+    static constexpr uint32_t T_P = APART ? 128 : 0, T_O = APART ? 192 : 256, T_ALL = 256 * NT;   // tile w: 128 w further
 };
 
-struct Shared {
-    uint64_t full[8], empty[8], s_full[2], p_full[2], pv_done[2];
+// behind the tiles
+template <int NT> struct Shared {
+    uint64_t q_full, full[8], empty[8], s_full[NT], s_read[NT], p_full[NT], pv_done[NT];
     uint32_t tmem;
     int abort;
 };
+template <int D> constexpr int smem_bytes() { return Cfg<D>::TILES + (int)sizeof(Shared<Cfg<D>::NT>); }
+static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 115712, "shared memory of an SM");
 
 struct Wait {
-    Shared* sh;
+    int* abort;
     int* err;
     long long timeout;
     // whole warps; false: gave up
@@ -83,11 +93,11 @@ struct Wait {
                 break;
             }
             if ((it & 63) == 63) {
-                if (*reinterpret_cast<volatile int*>(&sh->abort)) break;
+                if (*reinterpret_cast<volatile int*>(abort)) break;
                 const long long t = clock64();
                 if (t0 == 0) t0 = t;
                 else if (t - t0 > timeout) {
-                    *reinterpret_cast<volatile int*>(&sh->abort) = 1;
+                    *reinterpret_cast<volatile int*>(abort) = 1;
                     atomicCAS(err, 0, site);
                     break;
                 }
@@ -102,6 +112,12 @@ __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, long long 
     const long long t0 = clock64();
     while (!mbar_try_wait(smem_u32(bar), parity) && clock64() - t0 < cycles) {
     }
+}
+
+// one arrival for the warp, after what all its lanes did
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(bar));
 }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, uint32_t bar) {
@@ -132,82 +148,101 @@ __device__ __forceinline__ void st_v4(uint32_t addr, uint32_t a, uint32_t b, uin
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+__device__ __forceinline__ uint4 ld_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
 template <int D, int SRC>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::PER_SM)
 attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __grid_constant__ AttnArgs a, const int tok_first) {
     using C = Cfg<D>;
-    constexpr int NS = C::NS;
+    constexpr int NS = C::NS, NT = C::NT, MMA_WARP = 4 * NT;
     constexpr int NPROD = SRC == kPagedE4m3 ? 96 : 1;   // arrivals that complete a slot
-    extern __shared__ uint8_t dyn_raw[];
-    __shared__ Shared sh;
+    extern __shared__ __align__(1024) uint8_t dyn_raw[];
+    Shared<NT>& sh = *reinterpret_cast<Shared<NT>*>(dyn_raw + C::TILES);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     RowTile t;
-    if (!find_tile(a, blockIdx.x, 2 * BM, a.causal, t)) return;
+    if (!find_tile(a, blockIdx.x, NT * BM, a.causal, t)) return;
     const int hk = blockIdx.y, split = blockIdx.z;
     const int total_rows = t.nq * a.G;
-    const uint32_t base = (smem_u32(dyn_raw) + 1023u) & ~1023u;
-    const uint32_t s_ring = base + 2 * C::QBYTES;
+    const uint32_t base = smem_u32(dyn_raw);
+    const uint32_t s_ring = base + NT * C::QBYTES;
 
     // key tiles of each row tile: [jb, je[w])
-    int je[2], jb;
+    int je[NT], jb, jmax = 0;
     {
-        int n[2];
+        int most = 0;
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
+        for (int w = 0; w < NT; ++w) {
             const int first = t.row0 + w * BM, last = min(first + BM, total_rows) - 1;
-            n[w] = first < total_rows ? (keys_seen(a, t, last / a.G) + BN - 1) / BN : 0;
+            je[w] = first < total_rows ? (keys_seen(a, t, last / a.G) + BN - 1) / BN : 0;
+            most = max(most, je[w]);
         }
-        const int most = max(n[0], n[1]), per = (most + a.splits - 1) / a.splits;
+        const int per = (most + a.splits - 1) / a.splits;
         jb = split * per;
-        je[0] = max(jb, min(n[0], jb + per));
-        je[1] = max(jb, min(n[1], jb + per));
+#pragma unroll
+        for (int w = 0; w < NT; ++w) {
+            je[w] = max(jb, min(je[w], jb + per));
+            jmax = max(jmax, je[w]);
+        }
     }
-    const int jmax = max(je[0], je[1]);
-    const Wait wait{&sh, a.err, a.timeout};
+    const Wait wait{&sh.abort, a.err, a.timeout};
 
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(smem_u32(&sh.full[i]), NPROD);
             mbar_init(smem_u32(&sh.empty[i]), 1);
         }
-        for (int w = 0; w < 2; ++w) {
+        mbar_init(smem_u32(&sh.q_full), 4 * NT);
+        for (int w = 0; w < NT; ++w) {
             mbar_init(smem_u32(&sh.s_full[w]), 1);
-            mbar_init(smem_u32(&sh.p_full[w]), BM);
+            mbar_init(smem_u32(&sh.s_read[w]), 4);
+            mbar_init(smem_u32(&sh.p_full[w]), 4);
             mbar_init(smem_u32(&sh.pv_done[w]), 1);
         }
         sh.abort = 0;
         fence_mbar_init();
     }
-    if (warp == 8) {
-        tmem_alloc(smem_u32(&sh.tmem), 512);
+    if (warp == MMA_WARP) {
+        tmem_alloc(smem_u32(&sh.tmem), C::T_ALL);
         tmem_relinquish();
     }
-    // queries: rows beyond the last are zeros
-    if (tid < 256) {
-        for (int i = tid; i < 2 * BM * (D / 8); i += 256) {
-            const int r = i / (D / 8), c = i % (D / 8), row = t.row0 + r;
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (row < total_rows)
-                x = *reinterpret_cast<const uint4*>(a.q.p + (t.q0 + row / a.G) * a.q.st +
-                                                    (int64_t)(hk * a.G + row % a.G) * a.q.sh + c * 16);
-            st_v4(base + (r >> 7) * C::QBYTES + tile_off(r & 127, c), x.x, x.y, x.z, x.w);
-        }
-    }
-    fence_proxy_async();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
 
-    if (warp < 8) {
+    if (warp < MMA_WARP) {
         // ------------------------------------------------------------ softmax
-        regs_up<REGS_SOFTMAX>();
-        const int w = warp >> 2;
-        const int row = t.row0 + w * BM + (tid & 127);
-        const int seen = row < total_rows ? keys_seen(a, t, row / a.G) : 0;
+        regs_up<C::REGS_SOFTMAX>();
+        const int w = warp >> 2, trow = tid & 127, wrow = trow & ~31;   // tile, row of it, the warp's first
+        const int row = t.row0 + w * BM + trow;
+        const bool live = row < total_rows;
+        const int64_t tok = t.q0 + (live ? row / a.G : 0);
+        const int h = hk * a.G + (live ? row % a.G : 0);
+        const int seen = live ? keys_seen(a, t, row / a.G) : 0;
+        const int live_rows = min(32, total_rows - (row - lane));   // of the warp
+        const uint32_t q_tile = base + w * C::QBYTES;
+        constexpr int CPR = D / 8, RPI = 32 / CPR;   // 16-byte chunks of a row, rows of one instruction
+        {
+            // the warp's queries, a row's chunks on neighbouring lanes; rows beyond the last are zeros
+            const char* mine = a.q.p + tok * a.q.st + (int64_t)h * a.q.sh;
+#pragma unroll
+            for (int i = 0; i < 32 / RPI; ++i) {
+                const int r = RPI * i + lane / CPR, c = lane % CPR;
+                const char* src = reinterpret_cast<const char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), r));
+                cp_async16(q_tile + tile_off(wrow + r, c), src + c * 16, r < live_rows);
+            }
+            cp_async_commit();
+            cp_async_wait<0>();
+            fence_proxy_async();
+            warp_arrive(&sh.q_full);
+        }
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t ts = tmem + 128 * w + lanes, to = tmem + T_O + 128 * w + lanes;
+        const uint32_t ts = tmem + 128 * w + lanes, tp = ts + C::T_P, to = ts + C::T_O;
         const float sc = a.scale_log2;
         float m = -INFINITY, l = 0.f;   // m: reference of the exponents (unscaled score units)
         bool ok = true;
@@ -221,6 +256,11 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             tmem_wait_ld();
 #pragma unroll
             for (int c = 0; c < 4; ++c) reg_fence(s[c]);
+            if (C::APART) {   // the next scores may come
+                tc_fence_before();
+                warp_arrive(&sh.s_read[w]);
+            }
+            bool ended = j == jb;             // the previous product has
             const int left = seen - j * BN;   // keys of this tile that the row sees
             if (__any_sync(0xffffffffu, left < BN)) {
 #pragma unroll
@@ -228,92 +268,114 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 #pragma unroll
                     for (int i = 0; i < 32; ++i) s[c][i] = 32 * c + i < left ? s[c][i] : -INFINITY;
             }
-            float mx[4];
+            float mx[4];   // four chains of dependent maxima
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                mx[c] = fmax3_nan(s[c][0], s[c][1], s[c][2]);
+            for (int c = 0; c < 4; ++c) mx[c] = -INFINITY;
 #pragma unroll
-                for (int i = 3; i < 31; i += 2) mx[c] = fmax3_nan(mx[c], s[c][i], s[c][i + 1]);
-            }
-            const float mt = fmax3_nan(fmax3_nan(mx[0], mx[1], mx[2]), mx[3], fmax3_nan(s[0][31], s[1][31], fmax3_nan(s[2][31], s[3][31], s[3][31])));
+            for (int i = 0; i < 32; i += 2)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) mx[c] = fmax3_nan(mx[c], s[c][i], s[c][i + 1]);
+            const float mt = fmax3_nan(fmax3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]);
             // a score that is NaN or +inf: the row's result is NaN, whatever becomes of its weights
             if (!(mt < INFINITY)) l = __uint_as_float(0x7fc00000u);
             const float mn = fmaxf(m, mt);
             // raise the reference only when it has grown by more than 2^8 (or was -inf)
             const bool raise = (mn - m) * sc > 8.0f;
             if (__any_sync(0xffffffffu, raise)) {
-                const float f = raise ? exp2f((m - mn) * sc) : 1.0f;
+                const float f = raise ? ex2((m - mn) * sc) : 1.0f;
                 if (raise) m = mn;
                 l *= f;
-                if (j > jb) {
-                    if (!(ok = wait(&sh.pv_done[w], (j - jb - 1) & 1, 2))) break;
+                if (!ended) {
+                    if (!(ok = wait(&sh.pv_done[w], par ^ 1, 2))) break;
                     tc_fence_after();
+                    ended = true;
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        float o[32];
-                        tmem_ld32(to + 32 * c, o);
+                    for (int c = 0; c < D / 16; ++c) {
+                        float o[16];
+                        tmem_ld16(to + 16 * c, o);
                         tmem_wait_ld();
-                        reg_fence(o);
-                        uint32_t u[32];
+                        reg_fence16(o);
+                        uint32_t u[16];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(o[i] * f);
-                        tmem_st32(to + 32 * c, u);
+                        for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(o[i] * f);
+                        tmem_st16(to + 16 * c, u);
                     }
                     tmem_wait_st();
                 }
             }
             const float ref = m == -INFINITY ? 0.f : m * sc;
             const uint64_t sc2 = f32x2(sc, sc), ref2 = f32x2(-ref, -ref);
-            uint64_t sum = f32x2(0.f, 0.f);
+            uint64_t sum[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
             // Of every 8 pairs POLY are computed on the FMA pipe: the special-function unit alone takes as
             // long for a tile as the matrix products at D = 128, twice as long at D = 64.  Masked scores, and
             // rows that have seen none above -inf, need exact zeros: no polynomials there.
             const bool plain = __any_sync(0xffffffffu, left < BN || m == -INFINITY);
             auto weights = [&](auto poly) {
                 constexpr int POLY = decltype(poly)::value;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t p[16];
+                auto exps = [&](int c) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const uint64_t x = fma_f32x2(f32x2(s[c][2 * i], s[c][2 * i + 1]), sc2, ref2);
-                        uint64_t e;
-                        if (i % 8 < POLY) e = exp2_pair_poly(x);
+                        float x0, x1;
+                        if (i % 8 < POLY) f32x2_split(exp2_pair_poly(x), s[c][2 * i], s[c][2 * i + 1]);
                         else {
-                            float x0, x1;
                             f32x2_split(x, x0, x1);
-                            e = f32x2(ex2(x0), ex2(x1));
+                            s[c][2 * i] = ex2(x0);
+                            s[c][2 * i + 1] = ex2(x1);
                         }
-                        sum = add_f32x2(sum, e);
-                        float e0, e1;
-                        f32x2_split(e, e0, e1);
-                        p[i] = pack_bf16(e0, e1);
                     }
-                    tmem_st16(ts + 16 * c, p);
+                };
+                exps(0);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (c < 3) exps(c + 1);   // the next exponentials on their way before these are used
+                    uint32_t p[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        sum[i & 1] = add_f32x2(sum[i & 1], f32x2(s[c][2 * i], s[c][2 * i + 1]));
+                        p[i] = pack_bf16(s[c][2 * i], s[c][2 * i + 1]);
+                    }
+                    if (C::APART && c == 0 && !ended) {   // the previous weights are still being read
+                        if (!(ok = wait(&sh.pv_done[w], par ^ 1, 2))) return;
+                        tc_fence_after();
+                    }
+                    tmem_st16(tp + 16 * c, p);
                 }
             };
             if (plain) weights(std::integral_constant<int, 0>{});
             else weights(std::integral_constant<int, D == 64 ? VDM_POLY64 : VDM_POLY128>{});
+            if (!ok) break;
             float s0, s1;
-            f32x2_split(sum, s0, s1);
+            f32x2_split(add_f32x2(sum[0], sum[1]), s0, s1);
             l += s0 + s1;
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(smem_u32(&sh.p_full[w]));
+            warp_arrive(&sh.p_full[w]);
         }
         // ------------------------------------------------------------ output
         const int cnt = je[w] - jb;
         if (ok && cnt > 0) ok = wait(&sh.pv_done[w], (cnt - 1) & 1, 3);
         tc_fence_after();
-        if (ok && __any_sync(0xffffffffu, row < total_rows)) {
+        if (ok && live_rows > 0) {
             const float inv = l == 0.f ? 0.f : 1.0f / l;
             const float lse2 = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m * sc) + log2f(l);
-            const bool live = row < total_rows;
-            const int64_t tok = t.q0 + (live ? row / a.G : 0);
-            const int h = hk * a.G + (live ? row % a.G : 0);
             const int64_t prow = ((int64_t)split * a.Tq + tok) * a.Hq + h;
-            char* dst = a.splits > 1 ? reinterpret_cast<char*>(a.part_o + prow * D) : a.out.p + tok * a.out.st + h * a.out.sh;
+            const bool parts = a.splits > 1;
+            char* mine = parts ? reinterpret_cast<char*>(a.part_o + prow * D) : a.out.p + tok * a.out.st + h * a.out.sh;
             bool finite = true;
+            // The tile's queries are no longer read: their place takes the rows (as bf16, or half of each as
+            // fp32), so that they leave with a row's chunks on neighbouring lanes.
+            auto leave = [&](int bytes) {
+                __syncwarp();
+#pragma unroll 4
+                for (int i = 0; i < 32 / RPI; ++i) {
+                    const int r = RPI * i + lane / CPR, c = lane % CPR;
+                    char* dst = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), r));
+                    const uint4 v = ld_v4(q_tile + tile_off(wrow + r, c));
+                    if (r < live_rows) *reinterpret_cast<uint4*>(dst + bytes + c * 16) = v;
+                }
+                __syncwarp();
+            };
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 float o[32];
@@ -327,21 +389,22 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     o[i] = l == 0.f ? 0.f : o[i] * inv;
                     finite = finite && fabsf(o[i]) < INFINITY;
                 }
-                if (!live) continue;
-                if (a.splits > 1) {
+                if (parts) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        *reinterpret_cast<float4*>(dst + (32 * c + i) * 4) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    for (int i = 0; i < 8; ++i)
+                        st_v4(q_tile + tile_off(trow, (8 * c + i) % CPR), __float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]),
+                              __float_as_uint(o[4 * i + 2]), __float_as_uint(o[4 * i + 3]));
+                    if ((8 * c + 8) % CPR == 0) leave(((8 * c + 8) / CPR - 1) * CPR * 16);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8)
-                        *reinterpret_cast<uint4*>(dst + (32 * c + i) * 2) =
-                            make_uint4(pack_bf16(o[i], o[i + 1]), pack_bf16(o[i + 2], o[i + 3]), pack_bf16(o[i + 4], o[i + 5]),
-                                       pack_bf16(o[i + 6], o[i + 7]));
+                    for (int i = 0; i < 4; ++i)
+                        st_v4(q_tile + tile_off(trow, 4 * c + i), pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
+                              pack_bf16(o[8 * i + 4], o[8 * i + 5]), pack_bf16(o[8 * i + 6], o[8 * i + 7]));
                 }
             }
+            if (!parts) leave(0);
             if (live) {
-                if (a.splits > 1) a.part_lse[prow] = lse2;
+                if (parts) a.part_lse[prow] = lse2;
                 else if (a.lse) a.lse[tok * a.Hq + h] = lse2 * kLn2;
             }
             // a row that masked keys of its tiles and is not finite: again over its own keys
@@ -350,26 +413,20 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 const int src = __ffs(again) - 1;
                 again &= again - 1;
                 const int r = __shfl_sync(0xffffffffu, row, src), end = __shfl_sync(0xffffffffu, seen, src);
-                const int64_t pr = __shfl_sync(0xffffffffu, prow, src);
+                char* dst = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), src));
                 float4 o;
-                const float lg = repair_row<typename std::conditional<SRC == kPagedE4m3, uint8_t, __nv_bfloat16>::type, D, SRC != kPacked>(
+                repair_row<typename std::conditional<SRC == kPagedE4m3, uint8_t, __nv_bfloat16>::type, D, SRC != kPacked>(
                     a, t, hk, r, jb * BN, min(end, je[w] * BN), o);
-                const int64_t rt = t.q0 + r / a.G;
-                const int rh = hk * a.G + r % a.G;
                 if (4 * lane < D) {
-                    if (a.splits > 1) store4(a.part_o + pr * D + 4 * lane, o);
-                    else store4(reinterpret_cast<__nv_bfloat16*>(a.out.p + rt * a.out.st + rh * a.out.sh) + 4 * lane, o);
-                }
-                if (lane == 0) {
-                    if (a.splits > 1) a.part_lse[pr] = lg;
-                    else if (a.lse) a.lse[rt * a.Hq + rh] = lg * kLn2;
+                    if (parts) store4(reinterpret_cast<float*>(dst) + 4 * lane, o);
+                    else store4(reinterpret_cast<__nv_bfloat16*>(dst) + 4 * lane, o);
                 }
             }
         }
         tc_fence_before();
     } else {
-      regs_down<REGS_OTHER>();
-      if (warp == 8) {
+      regs_down<C::REGS_OTHER>();
+      if (warp == MMA_WARP) {
         // ------------------------------------------------------------ MMA issue
         constexpr uint32_t id_s = idesc_bf16(BM, BN, false), id_o = idesc_bf16(BM, D, true);
         const int n = jmax - jb;
@@ -382,16 +439,34 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             }
             mma_commit_w(smem_u32(&sh.s_full[w]));
         };
-        bool ok = true;
-        if (n > 0 && (ok = wait(&sh.full[0], 0, 4))) {
+        auto issue_pv = [&](int w, int i, uint32_t slot) {
+            if (!wait(&sh.p_full[w], i & 1, 6)) return false;
+            tc_fence_after();
+            const uint64_t dv = desc_v(s_ring + slot * C::SLOT);
+#pragma unroll
+            for (int kk = 0; kk < BN / 16; ++kk)
+                mma_ts_w(tmem + C::T_O + 128 * w, tmem + C::T_P + 128 * w + 8 * kk, dv + 128 * kk, id_o, i > 0 || kk > 0);
+            mma_commit_w(smem_u32(&sh.pv_done[w]));
+            return true;
+        };
+        bool ok = wait(&sh.q_full, 0, 12);
+        if (ok && n > 0 && (ok = wait(&sh.full[0], 0, 4))) {
             tc_fence_after();
 #pragma unroll
-            for (int w = 0; w < 2; ++w)
+            for (int w = 0; w < NT; ++w)
                 if (je[w] > jb) issue_s(w, 0);
             mma_commit_w(smem_u32(&sh.empty[0]));
         }
         for (int i = 0; ok && i < n; ++i) {
             const uint32_t iv = 2 * i + 1, ik = 2 * i + 2, sv = iv % NS, sk = ik % NS;
+            const bool more = i + 1 < n;
+            if (C::APART && more) {
+                // the next scores, as soon as these have been read
+                if (!(ok = wait(&sh.full[sk], (ik / NS) & 1, 7)) || !(ok = wait(&sh.s_read[0], i & 1, 10))) break;
+                tc_fence_after();
+                issue_s(0, sk);
+                mma_commit_w(smem_u32(&sh.empty[sk]));
+            }
             if (!(ok = wait(&sh.full[sv], (iv / NS) & 1, 5))) break;
             const int valid = t.nk - (jb + i) * BN;
             if (SRC != kPagedE4m3 && valid < BN) {
@@ -402,21 +477,12 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 fence_proxy_async();
                 __syncwarp();
             }
-            const bool more = i + 1 < n;
             bool have_k = false;
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
+            for (int w = 0; w < NT; ++w) {
                 if (!ok) break;
-                if (jb + i < je[w]) {
-                    if (!(ok = wait(&sh.p_full[w], i & 1, 6))) break;
-                    tc_fence_after();
-                    const uint64_t dv = desc_v(s_ring + sv * C::SLOT);
-#pragma unroll
-                    for (int kk = 0; kk < BN / 16; ++kk)
-                        mma_ts_w(tmem + T_O + 128 * w, tmem + 128 * w + 8 * kk, dv + 128 * kk, id_o, i > 0 || kk > 0);
-                    mma_commit_w(smem_u32(&sh.pv_done[w]));
-                }
-                if (jb + i + 1 < je[w]) {
+                if (jb + i < je[w] && !(ok = issue_pv(w, i, sv))) break;
+                if (!C::APART && jb + i + 1 < je[w]) {
                     if (!have_k) {
                         if (!(ok = wait(&sh.full[sk], (ik / NS) & 1, 7))) break;
                         tc_fence_after();
@@ -427,11 +493,11 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             }
             if (!ok) break;
             mma_commit_w(smem_u32(&sh.empty[sv]));
-            if (more) mma_commit_w(smem_u32(&sh.empty[sk]));
+            if (!C::APART && more) mma_commit_w(smem_u32(&sh.empty[sk]));
         }
     } else if (SRC != kPagedE4m3) {
         // ------------------------------------------------------------ TMA loads
-        if (warp == 9) {
+        if (warp == MMA_WARP + 1) {
             const int items = 2 * (jmax - jb);   // K_0 V_0 K_1 V_1 ...
             int issued = 0;
             for (; issued < items; ++issued) {
@@ -471,7 +537,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         }
     } else {
         // ------------------------------------------------------------ 8-bit tiles widened to bf16
-        const int ct = tid - 288;   // 0..95
+        const int ct = tid - 32 * (MMA_WARP + 1);   // 0..95
         for (int it = 0; it < 2 * (jmax - jb); ++it) {
             const int slot = it % NS, j0 = (jb + (it >> 1)) * BN;
             if (it >= NS && !wait(&sh.empty[slot], ((it / NS) - 1) & 1, 9)) break;
@@ -508,14 +574,14 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 
     // MMAs in flight read shared memory and write TMEM: wait for the last ones before either goes
     __syncthreads();
-    if (warp == 8) {
+    if (warp == MMA_WARP) {
         mma_commit_w(smem_u32(&sh.s_full[0]));   // completes once every MMA issued so far has; the barrier has no waiter left
         const int used = max(0, je[0] - jb);
         if (sh.abort == 0) drain(&sh.s_full[0], used & 1, a.timeout);
         else for (long long t0 = clock64(); clock64() - t0 < 2000000;) {   // gave up: phases unknown, MMAs end by themselves
         }
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(tmem, C::T_ALL);
     }
 }
 
@@ -559,9 +625,9 @@ template <int D, int SRC>
 vdm_status launch(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, bool tok_first, cudaStream_t s) {
     auto kern = attention_tc_kernel<D, SRC>;
     static std::atomic<uint64_t> ready{0};
-    VDM_TRY(prepare_kernel(ready, reinterpret_cast<const void*>(kern), Cfg<D>::SMEM));
-    const int64_t tiles = (a.Tq * a.G + (a.B < a.Tq ? a.B : a.Tq) * (int64_t)(2 * BM - 1)) / (2 * BM);
-    kern<<<dim3((unsigned)tiles, a.Hk, a.splits), THREADS, Cfg<D>::SMEM, s>>>(mk, mv, a, tok_first);
+    VDM_TRY(prepare_kernel(ready, reinterpret_cast<const void*>(kern), smem_bytes<D>()));
+    const int64_t tiles = (a.Tq * a.G + (a.B < a.Tq ? a.B : a.Tq) * (int64_t)(tc_rows(D) - 1)) / tc_rows(D);
+    kern<<<dim3((unsigned)tiles, a.Hk, a.splits), Cfg<D>::THREADS, smem_bytes<D>(), s>>>(mk, mv, a, tok_first);
     VDM_TRY(check_launch("attention_tc_kernel"));
     return a.splits > 1 ? launch_combine(a, VDM_BF16, s) : VDM_OK;
 }

@@ -135,7 +135,7 @@ Plan plan_attention(const vdm_attention* at, int B, int64_t Tq, int64_t max_kv) 
     // Row tiles of the kernel, blocks that run at once, and the cost of a block in key tiles: its
     // own share of the keys and a start and end worth about two tiles.  The number of splits is
     // the one with the shortest sum over waves; joining s parts costs about s rows' writing and reading.
-    const int64_t M = p.kernel == kTc ? 256 : 64, N = p.kernel == kTc ? 128 : 64, at_once = p.kernel == kTc ? 148 : 296;
+    const int64_t M = p.kernel == kTc ? tc_rows(at->D) : 64, N = p.kernel == kTc ? 128 : 64, at_once = p.kernel == kTc ? 148 * tc_per_sm(at->D) : 296;
     const int64_t tiles = (Tq * G + seqs * (M - 1)) / M * at->Hk, nk = (max_kv + N - 1) / N;
     double best = 0;
     for (int s = 1; s <= 64 && s * 2 <= (nk > 2 ? nk : 2); ++s) {

@@ -246,6 +246,10 @@ __device__ __forceinline__ float repair_row(const AttnArgs& a, const RowTile& t,
 // rows of a tile of the few-rows kernel
 inline int rows_tile(int G, int64_t Tq, int B) { return Tq * G <= 8 * (B < Tq ? B : Tq) ? 8 : 16; }
 
+// query rows of a block of the tensor-core kernel, and such blocks on an SM
+__host__ __device__ constexpr int tc_rows(int D) { return D == 64 ? 128 : 256; }
+constexpr int tc_per_sm(int D) { return D == 64 ? 2 : 1; }
+
 // Shared memory size (and clusters of 16 blocks) of a kernel, set once per device.
 inline vdm_status prepare_kernel(std::atomic<uint64_t>& ready, const void* f, int smem, bool clusters = false) {
     int dev = 0;
