@@ -26,6 +26,14 @@
 // D = 64 (256 columns): S [0,128) P [128,192) O [192,256), and the next scores are computed while the
 // softmax of these runs.
 //
+// What bounds it (measured with clocks in the kernel, 128 x 128 scores): D = 64, the special-function unit: a
+// tile takes 1024 cycles of its exponentials, two CTAs of an SM 2840 a step.  D = 128: the chain scores ->
+// softmax -> P V -> next scores, 3390 cycles a step of two tiles, 2050 of them matrix products.
+// Measured and not kept: a quarter of the exponentials by a polynomial on the FMA pipe (23 issue slots a
+// pair against 16 cycles of the unit: 1 % at D = 64, a loss at 128); two threads per row; one S for both
+// tiles, P apart (its users wait for one another: 3670 cycles); steps of 64 keys, S in two halves
+// (a 128 x 64 x 16 MMA takes as long as a 128 x 128 x 16 one).
+//
 // Masked keys: a key that a row does not see has weight 0.  V rows behind the sequence's end
 // are zeroed in shared memory (0 * NaN would reach every row); V rows inside the sequence that
 // only later queries see can still bring 0 * NaN or 0 * inf, so that a row which ends up not
@@ -47,10 +55,6 @@ namespace {
 using namespace ptx;
 
 constexpr int BM = 128, BN = 128;
-#ifndef VDM_POLY64
-#define VDM_POLY64 1
-#define VDM_POLY128 1
-#endif
 enum Source : int { kPacked = 0, kPagedBf16 = 1, kPagedE4m3 = 2 };
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -66,12 +70,13 @@ template <int D> struct Cfg {
     static constexpr int NS = D == 128 ? 5 : 6;      // slots beside the query tiles in 227 KB (113 KB)
     static constexpr int TILES = NT * QBYTES + NS * SLOT;
     static constexpr bool APART = NT == 1;           // P has columns of its own
+    static constexpr bool EARLY = !APART;            // P V in two parts (372 us, in one 384, for 343 GFLOP of prompts)
     static constexpr uint32_t T_P = APART ? 128 : 0, T_O = APART ? 192 : 256, T_ALL = 256 * NT;   // tile w: 128 w further
 };
 
 // behind the tiles
 template <int NT> struct Shared {
-    uint64_t q_full, full[8], empty[8], s_full[NT], s_read[NT], p_full[NT], pv_done[NT];
+    uint64_t q_full, full[8], empty[8], s_full[NT], s_read[NT], p_half[NT], p_full[NT], pv_done[NT];
     uint32_t tmem;
     int abort;
 };
@@ -200,6 +205,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         for (int w = 0; w < NT; ++w) {
             mbar_init(smem_u32(&sh.s_full[w]), 1);
             mbar_init(smem_u32(&sh.s_read[w]), 4);
+            mbar_init(smem_u32(&sh.p_half[w]), 4);
             mbar_init(smem_u32(&sh.p_full[w]), 4);
             mbar_init(smem_u32(&sh.pv_done[w]), 1);
         }
@@ -274,10 +280,8 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 #pragma unroll
             for (int i = 0; i < 32; i += 2)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) mx[c] = fmax3_nan(mx[c], s[c][i], s[c][i + 1]);
-            const float mt = fmax3_nan(fmax3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]);
-            // a score that is NaN or +inf: the row's result is NaN, whatever becomes of its weights
-            if (!(mt < INFINITY)) l = __uint_as_float(0x7fc00000u);
+                for (int c = 0; c < 4; ++c) mx[c] = fmax3(mx[c], s[c][i], s[c][i + 1]);
+            const float mt = fmax3(fmax3(mx[0], mx[1], mx[2]), mx[3], mx[3]);
             const float mn = fmaxf(m, mt);
             // raise the reference only when it has grown by more than 2^8 (or was -inf)
             const bool raise = (mn - m) * sc > 8.0f;
@@ -306,44 +310,36 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             const float ref = m == -INFINITY ? 0.f : m * sc;
             const uint64_t sc2 = f32x2(sc, sc), ref2 = f32x2(-ref, -ref);
             uint64_t sum[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
-            // Of every 8 pairs POLY are computed on the FMA pipe: the special-function unit alone takes as
-            // long for a tile as the matrix products at D = 128, twice as long at D = 64.  Masked scores, and
-            // rows that have seen none above -inf, need exact zeros: no polynomials there.
-            const bool plain = __any_sync(0xffffffffu, left < BN || m == -INFINITY);
-            auto weights = [&](auto poly) {
-                constexpr int POLY = decltype(poly)::value;
-                auto exps = [&](int c) {
+            auto exps = [&](int c) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const uint64_t x = fma_f32x2(f32x2(s[c][2 * i], s[c][2 * i + 1]), sc2, ref2);
-                        float x0, x1;
-                        if (i % 8 < POLY) f32x2_split(exp2_pair_poly(x), s[c][2 * i], s[c][2 * i + 1]);
-                        else {
-                            f32x2_split(x, x0, x1);
-                            s[c][2 * i] = ex2(x0);
-                            s[c][2 * i + 1] = ex2(x1);
-                        }
-                    }
-                };
-                exps(0);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (c < 3) exps(c + 1);   // the next exponentials on their way before these are used
-                    uint32_t p[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        sum[i & 1] = add_f32x2(sum[i & 1], f32x2(s[c][2 * i], s[c][2 * i + 1]));
-                        p[i] = pack_bf16(s[c][2 * i], s[c][2 * i + 1]);
-                    }
-                    if (C::APART && c == 0 && !ended) {   // the previous weights are still being read
-                        if (!(ok = wait(&sh.pv_done[w], par ^ 1, 2))) return;
-                        tc_fence_after();
-                    }
-                    tmem_st16(tp + 16 * c, p);
+                for (int i = 0; i < 16; ++i) {
+                    float x0, x1;
+                    f32x2_split(fma_f32x2(f32x2(s[c][2 * i], s[c][2 * i + 1]), sc2, ref2), x0, x1);
+                    s[c][2 * i] = ex2(x0);
+                    s[c][2 * i + 1] = ex2(x1);
                 }
             };
-            if (plain) weights(std::integral_constant<int, 0>{});
-            else weights(std::integral_constant<int, D == 64 ? VDM_POLY64 : VDM_POLY128>{});
+            exps(0);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if (c < 3) exps(c + 1);   // the next exponentials on their way before these are used
+                uint32_t p[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    sum[i & 1] = add_f32x2(sum[i & 1], f32x2(s[c][2 * i], s[c][2 * i + 1]));
+                    p[i] = pack_bf16(s[c][2 * i], s[c][2 * i + 1]);
+                }
+                if (C::APART && c == 0 && !ended) {   // the previous weights are still being read
+                    if (!(ok = wait(&sh.pv_done[w], par ^ 1, 2))) break;
+                    tc_fence_after();
+                }
+                tmem_st16(tp + 16 * c, p);
+                if (C::EARLY && c == 1) {   // the product of the first 64 keys may start
+                    tmem_wait_st();
+                    tc_fence_before();
+                    warp_arrive(&sh.p_half[w]);
+                }
+            }
             if (!ok) break;
             float s0, s1;
             f32x2_split(add_f32x2(sum[0], sum[1]), s0, s1);
@@ -440,12 +436,17 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             mma_commit_w(smem_u32(&sh.s_full[w]));
         };
         auto issue_pv = [&](int w, int i, uint32_t slot) {
-            if (!wait(&sh.p_full[w], i & 1, 6)) return false;
+            if (!wait(C::EARLY ? &sh.p_half[w] : &sh.p_full[w], i & 1, 6)) return false;
             tc_fence_after();
             const uint64_t dv = desc_v(s_ring + slot * C::SLOT);
 #pragma unroll
-            for (int kk = 0; kk < BN / 16; ++kk)
+            for (int kk = 0; kk < BN / 16; ++kk) {
+                if (C::EARLY && kk == BN / 32) {
+                    if (!wait(&sh.p_full[w], i & 1, 6)) return false;
+                    tc_fence_after();
+                }
                 mma_ts_w(tmem + C::T_O + 128 * w, tmem + C::T_P + 128 * w + 8 * kk, dv + 128 * kk, id_o, i > 0 || kk > 0);
+            }
             mma_commit_w(smem_u32(&sh.pv_done[w]));
             return true;
         };
@@ -477,19 +478,15 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 fence_proxy_async();
                 __syncwarp();
             }
-            bool have_k = false;
+            if (!C::APART && more) {
+                if (!(ok = wait(&sh.full[sk], (ik / NS) & 1, 7))) break;
+                tc_fence_after();
+            }
 #pragma unroll
             for (int w = 0; w < NT; ++w) {
                 if (!ok) break;
                 if (jb + i < je[w] && !(ok = issue_pv(w, i, sv))) break;
-                if (!C::APART && jb + i + 1 < je[w]) {
-                    if (!have_k) {
-                        if (!(ok = wait(&sh.full[sk], (ik / NS) & 1, 7))) break;
-                        tc_fence_after();
-                        have_k = true;
-                    }
-                    issue_s(w, sk);
-                }
+                if (!C::APART && jb + i + 1 < je[w]) issue_s(w, sk);
             }
             if (!ok) break;
             mma_commit_w(smem_u32(&sh.empty[sv]));

@@ -132,15 +132,15 @@ Plan plan_attention(const vdm_attention* at, int B, int64_t Tq, int64_t max_kv) 
             while (p.splits < 16 && tiles * p.cluster * p.splits < 296 && p.splits * p.cluster * 32 < steps) p.splits *= 2;
         return p;
     }
-    // Row tiles of the kernel, blocks that run at once, and the cost of a block in key tiles: its
-    // own share of the keys and a start and end worth about two tiles.  The number of splits is
-    // the one with the shortest sum over waves; joining s parts costs about s rows' writing and reading.
+    // Row tiles of the kernel, blocks that run at once, and the cost of a block in steps of N keys: its
+    // own share of the keys, and a start and end that take as long as four steps.  Joining s parts writes
+    // and reads s rows of floats, at 9 MB a step.  The number of splits is the one with the shortest sum.
     const int64_t M = p.kernel == kTc ? tc_rows(at->D) : 64, N = p.kernel == kTc ? 128 : 64, at_once = p.kernel == kTc ? 148 * tc_per_sm(at->D) : 296;
     const int64_t tiles = (Tq * G + seqs * (M - 1)) / M * at->Hk, nk = (max_kv + N - 1) / N;
     double best = 0;
     for (int s = 1; s <= 64 && s * 2 <= (nk > 2 ? nk : 2); ++s) {
         const double waves = (double)((tiles * s + at_once - 1) / at_once);
-        const double cost = waves * ((double)((nk + s - 1) / s) + 2.0) + (s > 1 ? 2.0 + 0.25 * s * waves : 0.0);
+        const double cost = waves * ((double)((nk + s - 1) / s) + 4.0) + (s > 1 ? 2.0 + s * (double)(Tq * at->Hq * at->D * 8) / 9e6 : 0.0);
         if (s == 1 || cost < 0.95 * best) {
             best = cost;
             p.splits = s;

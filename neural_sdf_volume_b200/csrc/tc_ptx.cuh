@@ -367,12 +367,6 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-// The same, NaN if any input is.
-__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
-    float d;
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
 // Registers of a warpgroup's threads; the shares of a block's warpgroups add up to at most what it was launched with.
 template <int N>
 __device__ __forceinline__ void regs_up() {
