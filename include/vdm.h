@@ -448,8 +448,8 @@ VDM_API vdm_status vdm_surface_case_table(uint8_t* ntri, uint8_t* tri);
  *     row are contiguous, rows start on 16-byte boundaries (base pointer and
  *     strides), and rows do not overlap.  D is 64 or 128; dtype f32 or bf16.
  *   - Sequence b owns the tokens [cu[b], cu[b+1]) of a packed tensor (cu: B+1
- *     int32, device).  Tokens outside every sequence (behind cu[B]) are neither
- *     read nor written.  Offsets are clamped to [0, T]; a decreasing pair is an
+ *     int32, device).  Tokens outside every sequence (behind cu[B]) have no
+ *     influence and are not written.  Offsets are clamped to [0, T]; a decreasing pair is an
  *     empty sequence.  Nothing else about them is checked.
  *   - Sums, norms and softmax statistics are float32.                       */
 typedef struct {
@@ -492,7 +492,8 @@ typedef struct {
     int32_t num_pages, page_size;   /* page_size 16, 32, 64, 128 or 256          */
     int32_t H, D;
     void *k, *v;                    /* [num_pages][H][page_size][D]              */
-    /* E4M3 only: one scale 2^(s - 127) per row, [num_pages][H][page_size] bytes  */
+    /* E4M3 only: one scale 2^(s - 127) per row, [num_pages][H][page_size] bytes,
+     * s in 27..246 (what vdm_cache_write gives); 16-byte aligned like k and v    */
     uint8_t *k_scale, *v_scale;
 } vdm_kv_cache;
 

@@ -31,18 +31,14 @@
 // only later queries of the tile see can bring 0 * NaN; see repair_row.
 #include <type_traits>
 
-#include "seq_internal.cuh"
-#include "tc_ptx.cuh"
+#include "attention_join.cuh"
 
 namespace vdm {
 namespace {
 
 using namespace ptx;
 
-constexpr int RM = 16;   // rows of a tile
-constexpr int RW = 4;    // warps of a block
 enum Source : int { kPacked = 0, kPagedBf16 = 1, kPagedE4m3 = 2 };
-constexpr float kLn2 = 0.69314718055994530942f;
 
 template <int D, int SRC> struct Cfg {
     static constexpr bool E8 = SRC == kPagedE4m3;
@@ -58,11 +54,6 @@ template <int D, int SRC> struct Cfg {
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
-}
 template <int W>
 __device__ __forceinline__ void lds128(uint32_t a, uint32_t (&v)[W]) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2 % W]), "=r"(v[3 % W]) : "r"(a));
@@ -76,17 +67,6 @@ __device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
     return v;
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t a) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t a) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
-    return v;
-}
-
 // D += A B, 16 x 8 x 16: fp16 or bf16 in, fp32 out
 template <bool HALF>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -123,29 +103,6 @@ template <int CH>
 __device__ __forceinline__ int swizzle_k(int r, int c) { return CH > 4 ? c ^ ((r & 1) << 2) : c; }
 template <int CH>
 __device__ __forceinline__ int swizzle_v(int r, int c) { return CH > 4 ? c ^ (((r >> 1) & 3) << 1) : c ^ (((r >> 1) & 1) << 1); }
-
-// A row's parts of the block's warps as one: maximum (result), sum and elements.
-template <int WARP>
-__device__ __forceinline__ float join_warps(const float (&sm)[RW][RM], const float (&sl)[RW][RM], uint32_t at, int row, bool on, float& L, float4& x) {
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < RW; ++w) M = fmaxf(M, sm[w][row]);
-    const float ref = M == -INFINITY ? 0.f : M;
-    L = 0.f;
-    x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < RW; ++w) {
-        const float pm = sm[w][row], pl = sl[w][row];
-        const float f = pm == -INFINITY && pl == 0.f ? 0.f : exp2f(pm - ref);
-        L = fmaf(f, pl, L);
-        if (on) {
-            const uint4 y = lds128(at + w * WARP);
-            x.x = fmaf(f, __uint_as_float(y.x), x.x), x.y = fmaf(f, __uint_as_float(y.y), x.y);
-            x.z = fmaf(f, __uint_as_float(y.z), x.z), x.w = fmaf(f, __uint_as_float(y.w), x.w);
-        }
-    }
-    return M;
-}
 
 // ROWS8: tiles have at most 8 rows, the other half of the matrix product's rows stays empty
 template <int D, int SRC, bool ROWS8>
@@ -280,7 +237,8 @@ __global__ void __launch_bounds__(RW * 32, 3) attention_rows_kernel(const __grid
 #pragma unroll
         for (int i = 0; i < KK; ++i) o[i][r][0] = o[i][r][1] = o[i][r][2] = o[i][r][3] = 0.f;
     }
-    constexpr float W0 = E8 ? 12.0f : 0.0f;   // fp16 weights are kept at 2^12 times their value
+    // fp16 weights are kept at 2^12 times their value; l, whose terms w 2^-e reach 2^(100 + 15), at 2^6
+    constexpr float W0 = E8 ? 12.0f : 0.0f, L0 = E8 ? 6.0f : 0.0f;
 
     int slot = 0, fill = NS - 1;
     for (int step = first; step < s1; step += stride) {
@@ -315,14 +273,15 @@ __global__ void __launch_bounds__(RW * 32, 3) attention_rows_kernel(const __grid
                 }
             }
         }
-        // in log2 units, with the value scale's exponent added; inv: 2^-exponent
+        // in log2 units, with the value scale's exponent added
         float inv[U][2];
         if (E8) {
             static_assert(!E8 || KS == 32, "a lane per key");
-            const uint32_t kb = lds_u8(bk + 2 * KS * RB + lane), vb = lds_u8(bk + 2 * KS * RB + KS + lane);
+            // value scales outside 2^-100 .. 2^119 are not valid; the zeros read for missing pages are among them
+            const uint32_t kb = lds_u8(bk + 2 * KS * RB + lane), vb = min(max(lds_u8(bk + 2 * KS * RB + KS + lane), 27u), 246u);
             const float f_ = scale_of((uint8_t)kb);
             const float ev_ = __uint_as_float(0x4b000000u | vb) - (8388608.0f + 127.0f);   // 2^23 + vb as a float
-            const float inv_ = __uint_as_float((uint32_t)max(1, 254 - (int)vb) << 23);     // beyond 253 not from vdm_cache_write
+            const float inv_ = __uint_as_float((248u - vb) << 23);   // 2^(-exponent - L0)
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -437,13 +396,13 @@ __global__ void __launch_bounds__(RW * 32, 3) attention_rows_kernel(const __grid
     __syncwarp();
 
     // the warp's rows into its ring
-    const float w0 = pow2i(-(int)W0);
+    const float w0 = pow2i(-(int)W0), l0 = pow2i((int)(L0 - W0));
 #pragma unroll
     for (int r = 0; r < NQ; ++r)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int row = 8 * r + 2 * t4 + j;
-            float x = l[r][j] * w0;
+            float x = l[r][j] * l0;
             x += __shfl_xor_sync(0xffffffffu, x, 4);
             x += __shfl_xor_sync(0xffffffffu, x, 8);
             x += __shfl_xor_sync(0xffffffffu, x, 16);
@@ -455,71 +414,8 @@ __global__ void __launch_bounds__(RW * 32, 3) attention_rows_kernel(const __grid
                 asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(ring + (row * D + d) * 4), "f"(o[i][r][j] * w0), "f"(o[i][r][2 + j] * w0) : "memory");
             }
         }
-    __syncthreads();
-
-    // joining: a row's parts in order, first the block's warps, then the cluster's blocks
-    const bool on = 4 * lane < D;
-    const uint32_t part = smem_u32(dyn);
-    if (cluster > 1) {
-        for (int row = warp; row < n_rows; row += RW) {
-            float L;
-            float4 x;
-            const float M = join_warps<C::WARP>(s_m, s_l, part + (row * D + 4 * lane) * 4, row, on, L, x);
-            __syncwarp();
-            if (on)
-                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(part + (row * D + 4 * lane) * 4), "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w) : "memory");
-            if (lane == 0) s_m[0][row] = M, s_l[0][row] = L;
-        }
-        cluster_sync();
-    }
-    for (int row = rank * RW + warp; row < n_rows; row += cluster * RW) {
-        float L = 0.f, ref;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (cluster == 1) {
-            const float M = join_warps<C::WARP>(s_m, s_l, part + (row * D + 4 * lane) * 4, row, on, L, x);
-            ref = M == -INFINITY ? 0.f : M;
-        } else {
-            // lane k: block k's maximum and sum
-            float pm = -INFINITY, pl = 0.f;
-            if (lane < cluster) {
-                pm = ld_cluster_f32(mapa(smem_u32(&s_m[0][row]), lane));
-                pl = ld_cluster_f32(mapa(smem_u32(&s_l[0][row]), lane));
-            }
-            float M = pm;
-#pragma unroll
-            for (int w = 16; w; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
-            ref = M == -INFINITY ? 0.f : M;
-            const float pf = pm == -INFINITY && pl == 0.f ? 0.f : exp2f(pm - ref);   // no key: nothing
-#pragma unroll 4
-            for (int k = 0; k < cluster; ++k) {
-                const float f = __shfl_sync(0xffffffffu, pf, k);
-                L = fmaf(f, __shfl_sync(0xffffffffu, pl, k), L);
-                if (on) {
-                    const float4 y = ld_cluster_f4(mapa(part + (row * D + 4 * lane) * 4, k));
-                    x.x = fmaf(f, y.x, x.x), x.y = fmaf(f, y.y, x.y), x.z = fmaf(f, y.z, x.z), x.w = fmaf(f, y.w, x.w);
-                }
-            }
-        }
-        const float inv = L == 0.f ? 0.f : 1.0f / L;
-        x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
-        float lse2 = L == 0.f ? -INFINITY : ref + log2f(L);
-        const int rr = t.row0 + row, see = keys_seen(a, t, rr / a.G);
-        const bool bad = !(fabsf(x.x) < INFINITY && fabsf(x.y) < INFINITY && fabsf(x.z) < INFINITY && fabsf(x.w) < INFINITY);
-        const int end = min(s1 * KS, most);
-        if (see < end && __any_sync(0xffffffffu, bad))
-            lse2 = repair_row<typename std::conditional<E8, uint8_t, __nv_bfloat16>::type, D, PAGED>(a, t, hk, rr, s0 * KS, min(see, end), x);
-        const int64_t tok = t.q0 + rr / a.G;
-        const int h = hk * a.G + rr % a.G;
-        if (a.splits > 1) {
-            const int64_t prow = ((int64_t)split * a.Tq + tok) * a.Hq + h;
-            if (on) store4(a.part_o + prow * D + 4 * lane, x);
-            if (lane == 0) a.part_lse[prow] = lse2;
-        } else {
-            if (on) store4(reinterpret_cast<__nv_bfloat16*>(a.out.p + tok * a.out.st + h * a.out.sh) + 4 * lane, x);
-            if (lane == 0 && a.lse) a.lse[tok * a.Hq + h] = lse2 * kLn2;
-        }
-    }
-    if (cluster > 1) cluster_sync();   // no block leaves while another reads its shared memory
+    join_rows<__nv_bfloat16, typename std::conditional<E8, uint8_t, __nv_bfloat16>::type, D, PAGED, C::WARP, true>(
+        a, t, hk, split, rank, cluster, n_rows, s0 * KS, min(s1 * KS, most), s_m, s_l, smem_u32(dyn));
 }
 
 template <int D, int SRC, bool ROWS8>
@@ -527,19 +423,9 @@ vdm_status launch(const AttnArgs& a, cudaStream_t s) {
     auto kern = attention_rows_kernel<D, SRC, ROWS8>;
     constexpr int M = ROWS8 ? 8 : RM;
     static std::atomic<uint64_t> ready{0};
-    VDM_TRY(prepare_kernel(ready, reinterpret_cast<const void*>(kern), Cfg<D, SRC>::SMEM, true));
+    VDM_TRY(prepare_kernel(ready, reinterpret_cast<const void*>(kern), Cfg<D, SRC>::SMEM));
     const int64_t tiles = (a.Tq * a.G + (a.B < a.Tq ? a.B : a.Tq) * (int64_t)(M - 1)) / M;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)tiles, a.Hk, a.splits * a.cluster);
-    cfg.blockDim = dim3(RW * 32);
-    cfg.dynamicSmemBytes = Cfg<D, SRC>::SMEM;
-    cfg.stream = s;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = 1, at.val.clusterDim.y = 1, at.val.clusterDim.z = a.cluster;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    VDM_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, a, a.cluster));
+    VDM_TRY(launch_cluster(kern, dim3((unsigned)tiles, a.Hk, a.splits * a.cluster), RW * 32, Cfg<D, SRC>::SMEM, a.cluster, s, a, a.cluster));
     VDM_TRY(check_launch("attention_rows_kernel"));
     return a.splits > 1 ? launch_combine(a, VDM_BF16, s) : VDM_OK;
 }

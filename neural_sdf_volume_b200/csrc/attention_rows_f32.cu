@@ -1,0 +1,169 @@
+// Attention of few query rows to many keys in float32: keys and values float32 (packed or paged)
+// or 8-bit.  Bound by memory for float32 keys.
+//
+// A tile is up to R = 4 rows (token, query head of the group) of one sequence and key head; its
+// keys are shared out over the warps of a cluster of blocks as in the bf16 kernel.  A warp takes four
+// keys at a time, eight lanes to a key with D / 8 elements each: a key's scores need three
+// shuffles a row where a key to the whole warp needs five, and q and o of the rows stay in
+// registers.  Each group of eight lanes runs the softmax on its own keys (maximum, sum,
+// o <- o 2^(m - m') + 2^(s - m') v); the four groups join at the end, then the warps and blocks.
+// A value row counts only for rows that see it, so that what masked keys hold has no influence.
+#include "attention_join.cuh"
+
+namespace vdm {
+namespace {
+
+template <typename TC, int D, bool PAGED, int R>
+__global__ void __launch_bounds__(RW * 32) attention_rows_f32_kernel(const __grid_constant__ AttnArgs a, const int cluster) {
+    constexpr bool E8 = sizeof(TC) == 1;
+    constexpr int NI = D / 32;            // groups of 4 elements of a lane
+    constexpr int WARP = R * D * 4;
+    __shared__ __align__(16) float s_part[RW][R][D];
+    __shared__ float s_m[RW][RM], s_l[RW][RM];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane >> 3, c = lane & 7;
+    RowTile t;
+    if (!find_tile(a, blockIdx.x, R, a.causal, t)) return;   // the whole cluster alike
+    const int hk = blockIdx.y, rank = blockIdx.z % cluster, split = blockIdx.z / cluster;
+    const int n_rows = min(R, t.nq * a.G - t.row0);
+    const int most = keys_seen(a, t, (t.row0 + n_rows - 1) / a.G);
+    const int n_steps = (most + 3) / 4, per = (n_steps + a.splits - 1) / a.splits;
+    const int s0 = min(n_steps, split * per), s1 = min(n_steps, s0 + per);
+    auto dim = [&](int i) { return E8 ? c * (D / 8) + 4 * i : 4 * (c + 8 * i); };   // a lane's i-th group of elements
+
+    float4 q[R][NI], o[R][NI];
+    float m[R], l[R];
+    int seen[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const bool on = r < n_rows;
+        const int rr = t.row0 + (on ? r : 0);
+        seen[r] = on ? keys_seen(a, t, rr / a.G) : 0;
+        const float* p = reinterpret_cast<const float*>(a.q.p + (t.q0 + rr / a.G) * a.q.st + (int64_t)(hk * a.G + rr % a.G) * a.q.sh);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            q[r][i] = load4f(p + dim(i));
+            o[r][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+    }
+    const KvRows<TC, PAGED> kv{a, t, hk};
+    for (int step = s0 + rank * RW + warp; step < s1; step += cluster * RW) {
+        const int key = 4 * step + j;
+        float4 k[NI], v[NI];
+        bool there = key < most;
+        if constexpr (PAGED) {
+            const int64_t row = there ? cache_row(a.c, t.b, hk, key) : -1;
+            if (row >= 0) {
+                const TC *pk = reinterpret_cast<const TC*>(a.c.k) + row * D, *pv = reinterpret_cast<const TC*>(a.c.v) + row * D;
+                float fk = 1.f, fv = 1.f;
+                if (E8) fk = scale_of(a.c.ks[row]), fv = scale_of(a.c.vs[row]);
+#pragma unroll
+                for (int i = 0; i < NI; ++i) k[i] = load4f(pk + dim(i)), v[i] = load4f(pv + dim(i));
+                if (E8)
+#pragma unroll
+                    for (int i = 0; i < NI; ++i) {
+                        k[i].x *= fk, k[i].y *= fk, k[i].z *= fk, k[i].w *= fk;
+                        v[i].x *= fv, v[i].y *= fv, v[i].z *= fv, v[i].w *= fv;
+                    }
+            } else {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) k[i] = v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                k[i] = v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (there) k[i] = kv.get(false, key, dim(i)), v[i] = kv.get(true, key, dim(i));
+            }
+        }
+        float s[R];
+        bool raise = false;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float x = 0.f;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) x = fmaf(q[r][i].x, k[i].x, fmaf(q[r][i].y, k[i].y, fmaf(q[r][i].z, k[i].z, fmaf(q[r][i].w, k[i].w, x))));
+            x += __shfl_xor_sync(0xffffffffu, x, 1);
+            x += __shfl_xor_sync(0xffffffffu, x, 2);
+            x += __shfl_xor_sync(0xffffffffu, x, 4);
+            s[r] = key < seen[r] ? x * a.scale_log2 : -INFINITY;
+            raise = raise || s[r] > m[r];
+        }
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float mn = fmaxf(m[r], s[r]), f = mn == -INFINITY ? 1.0f : exp2f(m[r] - mn);
+                m[r] = mn;
+                l[r] *= f;
+#pragma unroll
+                for (int i = 0; i < NI; ++i) o[r][i].x *= f, o[r][i].y *= f, o[r][i].z *= f, o[r][i].w *= f;
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (key >= seen[r]) continue;
+            const float p = exp2f(s[r] - (m[r] == -INFINITY ? 0.f : m[r]));
+            l[r] += p;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                o[r][i].x = fmaf(p, v[i].x, o[r][i].x), o[r][i].y = fmaf(p, v[i].y, o[r][i].y);
+                o[r][i].z = fmaf(p, v[i].z, o[r][i].z), o[r][i].w = fmaf(p, v[i].w, o[r][i].w);
+            }
+        }
+        __syncwarp();
+    }
+    // the four groups as one, in a fixed order
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+        for (int w = 8; w < 32; w <<= 1) {
+            const float mo = __shfl_xor_sync(0xffffffffu, m[r], w), lo = __shfl_xor_sync(0xffffffffu, l[r], w);
+            const float mn = fmaxf(m[r], mo), base = mn == -INFINITY ? 0.f : mn;
+            // a group without keys has m = -inf, l = 0, o = 0; its factor is 0
+            const float f = exp2f(m[r] - base), fo = exp2f(mo - base);
+            l[r] = l[r] * f + lo * fo;
+            m[r] = mn;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                o[r][i].x = o[r][i].x * f + __shfl_xor_sync(0xffffffffu, o[r][i].x, w) * fo;
+                o[r][i].y = o[r][i].y * f + __shfl_xor_sync(0xffffffffu, o[r][i].y, w) * fo;
+                o[r][i].z = o[r][i].z * f + __shfl_xor_sync(0xffffffffu, o[r][i].z, w) * fo;
+                o[r][i].w = o[r][i].w * f + __shfl_xor_sync(0xffffffffu, o[r][i].w, w) * fo;
+            }
+        }
+        if (lane == 0) s_m[warp][r] = m[r], s_l[warp][r] = l[r];
+        if (j == 0)
+#pragma unroll
+            for (int i = 0; i < NI; ++i) *reinterpret_cast<float4*>(&s_part[warp][r][dim(i)]) = o[r][i];
+    }
+    join_rows<float, TC, D, PAGED, WARP, false>(a, t, hk, split, rank, cluster, n_rows, 0, 0, s_m, s_l, ptx::smem_u32(&s_part[0][0][0]));
+}
+
+template <typename TC, int D, bool PAGED, int R>
+vdm_status launch(const AttnArgs& a, cudaStream_t s) {
+    auto kern = attention_rows_f32_kernel<TC, D, PAGED, R>;
+    static std::atomic<uint64_t> ready{0};
+    VDM_TRY(prepare_kernel(ready, reinterpret_cast<const void*>(kern), 0));
+    const int64_t tiles = (a.Tq * a.G + (a.B < a.Tq ? a.B : a.Tq) * (int64_t)(R - 1)) / R;
+    VDM_TRY(launch_cluster(kern, dim3((unsigned)tiles, a.Hk, a.splits * a.cluster), RW * 32, 0, a.cluster, s, a, a.cluster));
+    VDM_TRY(check_launch("attention_rows_f32_kernel"));
+    return a.splits > 1 ? launch_combine(a, VDM_F32, s) : VDM_OK;
+}
+
+template <typename TC, bool PAGED>
+vdm_status launch_d(const AttnArgs& a, cudaStream_t s) {
+    const int R = rows_tile_f32(a.G, a.Tq, a.B);
+    if (a.D == 64) return R == 1 ? launch<TC, 64, PAGED, 1>(a, s) : R == 2 ? launch<TC, 64, PAGED, 2>(a, s) : launch<TC, 64, PAGED, 4>(a, s);
+    return R == 1 ? launch<TC, 128, PAGED, 1>(a, s) : R == 2 ? launch<TC, 128, PAGED, 2>(a, s) : launch<TC, 128, PAGED, 4>(a, s);
+}
+
+}  // namespace
+
+vdm_status launch_attention_rows_f32(const AttnArgs& a, cudaStream_t s) {
+    if (a.paged ? a.c.num_pages == 0 || a.c.max_pages == 0 : a.Tk == 0) return launch_attention_simt(a, VDM_F32, s);   // no keys at all
+    if (!a.paged) return launch_d<float, false>(a, s);
+    return a.c.dtype == VDM_CACHE_E4M3 ? launch_d<uint8_t, true>(a, s) : launch_d<float, true>(a, s);
+}
+
+}  // namespace vdm

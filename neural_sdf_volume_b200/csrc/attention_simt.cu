@@ -4,9 +4,9 @@
 // A block takes 64 query rows (query heads of a group beside one another: row = token x
 // group) of one sequence and key head and runs over its keys in tiles of 64 with the running
 // maximum m and sum l of the softmax: o <- o 2^(m - m') + 2^(s - m') v, out = o / l, with
-// the scale and log2 e folded into s.  Thread (ty, tx) of 16 x 16 owns rows 4 ty .. 4 ty + 3 and
-// keys tx + 16 j of the scores, and columns 4 tx + 64 j of the output: 64 fused multiply-adds
-// per eight 16-byte shared loads.  Bound by the FMA pipe.
+// the scale and log2 e folded into s.  Thread (ty, tx) of 8 x 16 owns rows 8 ty .. 8 ty + 7 and
+// keys tx + 16 j of the scores, and columns 4 tx + 64 j of the output: 128 fused multiply-adds
+// for twelve 16-byte shared loads, eight of them the same for half a warp.  Bound by the FMA pipe.
 //
 // A key that a row does not see has score -inf and weight 0; since 0 * NaN would still reach
 // the row through the product with v, a value row that not every row of the tile may see is
@@ -16,11 +16,11 @@
 namespace vdm {
 namespace {
 
-constexpr int BR = 64, BK = 64, ST = 256;
+constexpr int BR = 64, BK = 64, ST = 128, TR = 8;   // TR: rows of a thread
 constexpr float kLn2 = 0.69314718055994530942f;
 
 template <typename T, typename TC, int D, bool PAGED>
-__global__ void __launch_bounds__(ST, 2) attention_simt_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(ST, D == 64 ? 3 : 2) attention_simt_kernel(const AttnArgs a) {
     constexpr int LD = D + 4, LP = BK + 4, NC = D / 64;
     extern __shared__ float4 smem4[];
     float* Qs = reinterpret_cast<float*>(smem4);
@@ -44,11 +44,11 @@ __global__ void __launch_bounds__(ST, 2) attention_simt_kernel(const AttnArgs a)
         }
         *reinterpret_cast<float4*>(Qs + r * LD + d) = x;
     }
-    int seen[4];
-    float m[4], l[4], o[4][NC][4];
+    int seen[TR];
+    float m[TR], l[TR], o[TR][NC][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = 4 * ty + i;
+    for (int i = 0; i < TR; ++i) {
+        const int r = TR * ty + i;
         seen[i] = r < n_rows ? keys_seen(a, t, (t.row0 + r) / a.G) : 0;
         m[i] = -INFINITY;
         l[i] = 0.f;
@@ -74,28 +74,27 @@ __global__ void __launch_bounds__(ST, 2) attention_simt_kernel(const AttnArgs a)
             *reinterpret_cast<float4*>(Vs + r * LD + d) = y;
         }
         __syncthreads();
-        float s[4][4] = {};
-#pragma unroll 4
+        float s[TR][4] = {};
+#pragma unroll 2
         for (int d = 0; d < D; d += 4) {
-            float4 qv[4], kk[4];
+            float4 kk[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                qv[i] = *reinterpret_cast<const float4*>(Qs + (4 * ty + i) * LD + d);
-                kk[i] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * i) * LD + d);
-            }
+            for (int j = 0; j < 4; ++j) kk[j] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * j) * LD + d);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < TR; ++i) {
+                const float4 qv = *reinterpret_cast<const float4*>(Qs + (TR * ty + i) * LD + d);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    s[i][j] = fmaf(qv[i].x, kk[j].x, s[i][j]);
-                    s[i][j] = fmaf(qv[i].y, kk[j].y, s[i][j]);
-                    s[i][j] = fmaf(qv[i].z, kk[j].z, s[i][j]);
-                    s[i][j] = fmaf(qv[i].w, kk[j].w, s[i][j]);
+                    s[i][j] = fmaf(qv.x, kk[j].x, s[i][j]);
+                    s[i][j] = fmaf(qv.y, kk[j].y, s[i][j]);
+                    s[i][j] = fmaf(qv.z, kk[j].z, s[i][j]);
+                    s[i][j] = fmaf(qv.w, kk[j].w, s[i][j]);
                 }
+            }
         }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < TR; ++i) {
             float mx = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -106,15 +105,13 @@ __global__ void __launch_bounds__(ST, 2) attention_simt_kernel(const AttnArgs a)
             for (int w = 1; w < 16; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
             const float mn = fmaxf(m[i], mx), base = mn == -INFINITY ? 0.f : mn;
             const float f = exp2f(m[i] - base);
-            float sum = 0.f;
+            float sum = 0.f;   // of this thread's keys; the row's at the end
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float p = exp2f(s[i][j] - base);
                 sum += p;
-                Ps[(4 * ty + i) * LP + tx + 16 * j] = p;
+                Ps[(TR * ty + i) * LP + tx + 16 * j] = p;
             }
-#pragma unroll
-            for (int w = 1; w < 16; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
             l[i] = l[i] * f + sum;
             m[i] = mn;
 #pragma unroll
@@ -128,30 +125,36 @@ __global__ void __launch_bounds__(ST, 2) attention_simt_kernel(const AttnArgs a)
         const bool masked = j0 + BK > least;
 #pragma unroll 2
         for (int j = 0; j < BK; j += 4) {
-            float4 p[4];
+            float4 v[4][NC];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(Ps + (4 * ty + i) * LP + j);
+            for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
-            for (int jj = 0; jj < 4; ++jj) {
+                for (int c = 0; c < NC; ++c) v[jj][c] = *reinterpret_cast<const float4*>(Vs + (j + jj) * LD + 64 * c + 4 * tx);
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    const float4 v = *reinterpret_cast<const float4*>(Vs + (j + jj) * LD + 64 * c + 4 * tx);
+            for (int i = 0; i < TR; ++i) {
+                const float4 p = *reinterpret_cast<const float4*>(Ps + (TR * ty + i) * LP + j);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float w = jj == 0 ? p[i].x : jj == 1 ? p[i].y : jj == 2 ? p[i].z : p[i].w;
-                        if (masked && j0 + j + jj >= seen[i]) continue;
-                        o[i][c][0] = fmaf(w, v.x, o[i][c][0]);
-                        o[i][c][1] = fmaf(w, v.y, o[i][c][1]);
-                        o[i][c][2] = fmaf(w, v.z, o[i][c][2]);
-                        o[i][c][3] = fmaf(w, v.w, o[i][c][3]);
+                for (int jj = 0; jj < 4; ++jj) {
+                    const float w = jj == 0 ? p.x : jj == 1 ? p.y : jj == 2 ? p.z : p.w;
+                    if (masked && j0 + j + jj >= seen[i]) continue;
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        o[i][c][0] = fmaf(w, v[jj][c].x, o[i][c][0]);
+                        o[i][c][1] = fmaf(w, v[jj][c].y, o[i][c][1]);
+                        o[i][c][2] = fmaf(w, v[jj][c].z, o[i][c][2]);
+                        o[i][c][3] = fmaf(w, v[jj][c].w, o[i][c][3]);
                     }
                 }
             }
         }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = 4 * ty + i;
+    for (int i = 0; i < TR; ++i)
+#pragma unroll
+        for (int w = 1; w < 16; w <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
+#pragma unroll
+    for (int i = 0; i < TR; ++i) {
+        const int r = TR * ty + i;
         if (r >= n_rows) continue;
         const int row = t.row0 + r;
         const int64_t tok = t.q0 + row / a.G;

@@ -14,7 +14,7 @@
 //                        tensor cores work on the other's (D = 64: on the other CTA's);
 //   warp 4 NT + 1        TMA loads of K and V tiles into a ring of slots (packed: one box of 128
 //                        tokens per 64 columns; paged: one box per page);
-//   warps 4 NT + 1 .. 3  (8-bit cache) instead read codes from global memory, widen them to bf16 -
+//   warps from 4 NT + 1  (8-bit cache) instead read codes from global memory, widen them to bf16 -
 //                        exact: a code times a power of two - and write the ring's slots.
 // The maximum that the exponents refer to follows the running maximum only when that has
 // grown by more than 8 (log2 units): then O and l are rescaled, which needs the previous
@@ -62,9 +62,12 @@ template <int D> struct Cfg {
     static constexpr int PANELS = D / 64;
     static constexpr int NT = tc_rows(D) / BM;       // row tiles of a CTA
     static constexpr int PER_SM = NT == 1 ? 2 : 1;
-    static constexpr int THREADS = 128 * NT + 128;
-    // registers a thread, out of 128 (two CTAs of 256 threads) or 168 (one of 384) at launch
-    static constexpr int REGS_SOFTMAX = NT == 1 ? 192 : 208, REGS_OTHER = NT == 1 ? 64 : 88;
+    // warps that widen 8-bit tiles: a tile of D = 128 keeps seven busy
+    static constexpr int WIDEN = NT == 1 ? 3 : 7;
+    static constexpr int threads(int src) { return 128 * NT + (src == kPagedE4m3 ? 32 + 32 * WIDEN : 128); }
+    // registers a thread, out of 128 at launch (two CTAs of 256 threads, one of 512) or 168 (one of 384)
+    static constexpr int regs_softmax(int src) { return threads(src) == 384 ? 208 : 192; }
+    static constexpr int regs_other(int src) { return threads(src) == 384 ? 88 : 64; }
     static constexpr int QBYTES = BM * D * 2;        // one query tile
     static constexpr int SLOT = BN * D * 2;          // one key or value tile
     static constexpr int NS = D == 128 ? 5 : 6;      // slots beside the query tiles in 227 KB (113 KB)
@@ -160,12 +163,12 @@ __device__ __forceinline__ uint4 ld_v4(uint32_t addr) {
 }
 
 template <int D, int SRC>
-__global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::PER_SM)
+__global__ void __launch_bounds__(Cfg<D>::threads(SRC), Cfg<D>::PER_SM)
 attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __grid_constant__ AttnArgs a, const int tok_first) {
     using C = Cfg<D>;
     constexpr int NS = C::NS, NT = C::NT, MMA_WARP = 4 * NT;
-    constexpr int NPROD = SRC == kPagedE4m3 ? 96 : 1;   // arrivals that complete a slot
+    constexpr int NPROD = SRC == kPagedE4m3 ? C::WIDEN : 1;   // arrivals that complete a slot
     extern __shared__ __align__(1024) uint8_t dyn_raw[];
     Shared<NT>& sh = *reinterpret_cast<Shared<NT>*>(dyn_raw + C::TILES);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -223,7 +226,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 
     if (warp < MMA_WARP) {
         // ------------------------------------------------------------ softmax
-        regs_up<C::REGS_SOFTMAX>();
+        regs_up<C::regs_softmax(SRC)>();
         const int w = warp >> 2, trow = tid & 127, wrow = trow & ~31;   // tile, row of it, the warp's first
         const int row = t.row0 + w * BM + trow;
         const bool live = row < total_rows;
@@ -421,7 +424,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         }
         tc_fence_before();
     } else {
-      regs_down<C::REGS_OTHER>();
+      regs_down<C::regs_other(SRC)>();
       if (warp == MMA_WARP) {
         // ------------------------------------------------------------ MMA issue
         constexpr uint32_t id_s = idesc_bf16(BM, BN, false), id_o = idesc_bf16(BM, D, true);
@@ -534,7 +537,8 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         }
     } else {
         // ------------------------------------------------------------ 8-bit tiles widened to bf16
-        const int ct = tid - 32 * (MMA_WARP + 1);   // 0..95
+        constexpr int CT = 32 * C::WIDEN;
+        const int ct = tid - 32 * (MMA_WARP + 1);
         for (int it = 0; it < 2 * (jmax - jb); ++it) {
             const int slot = it % NS, j0 = (jb + (it >> 1)) * BN;
             if (it >= NS && !wait(&sh.empty[slot], ((it / NS) - 1) & 1, 9)) break;
@@ -543,7 +547,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             const uint32_t dst = s_ring + slot * C::SLOT;
             constexpr int CH = D / 16;   // 16-code chunks of a row
 #pragma unroll 4
-            for (int x = ct; x < BN * CH; x += 96) {
+            for (int x = ct; x < BN * CH; x += CT) {
                 const int r = x / CH, c = x % CH;
                 const int64_t row = j0 + r < t.nk ? cache_row(a.c, t.b, hk, j0 + r) : -1;
                 uint4 u = make_uint4(0u, 0u, 0u, 0u);
@@ -564,7 +568,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 st_v4(dst + tile_off(r, 2 * c + 1), o[4], o[5], o[6], o[7]);
             }
             fence_proxy_async();
-            mbar_arrive(smem_u32(&sh.full[slot]));
+            warp_arrive(&sh.full[slot]);
         }
       }
     }
@@ -624,7 +628,7 @@ vdm_status launch(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& 
     static std::atomic<uint64_t> ready{0};
     VDM_TRY(prepare_kernel(ready, reinterpret_cast<const void*>(kern), smem_bytes<D>()));
     const int64_t tiles = (a.Tq * a.G + (a.B < a.Tq ? a.B : a.Tq) * (int64_t)(tc_rows(D) - 1)) / tc_rows(D);
-    kern<<<dim3((unsigned)tiles, a.Hk, a.splits), Cfg<D>::THREADS, smem_bytes<D>(), s>>>(mk, mv, a, tok_first);
+    kern<<<dim3((unsigned)tiles, a.Hk, a.splits), Cfg<D>::threads(SRC), smem_bytes<D>(), s>>>(mk, mv, a, tok_first);
     VDM_TRY(check_launch("attention_tc_kernel"));
     return a.splits > 1 ? launch_combine(a, VDM_BF16, s) : VDM_OK;
 }

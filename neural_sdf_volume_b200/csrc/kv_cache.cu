@@ -4,98 +4,144 @@
 // E4M3 row: e = min { e : max |x| <= 448 2^e }, code = rn(x 2^-e).  The scale is a power of
 // two, so that code * scale is exact in float32 and bf16 and a reader adds no rounding of
 // its own; the codes' relative precision is that of any other scale, since e4m3 is a
-// floating format (at most one binade of its 18 goes unused).  Bound by memory: an element
-// is read once and written once.  One warp per token and side (keys, values), all heads: the
-// token's sequence and page are looked up once.
+// floating format (at most one binade of its 18 goes unused).
+//
+// Bound by memory: an element is read once and written once.  One warp per token: its sequence and
+// page are looked up once for the keys and values of all heads (the sequence by counting offsets,
+// 32 at a time: one load's latency where a binary search has log2 B), and a lane has eight 16-byte
+// pieces under way; a writer asks for its first eight before the lookup.
 #include "seq_internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace vdm {
 namespace {
 
 constexpr int CT = 128;
 
-// sequence that owns token t (offsets ascending): the largest b with cu[b] <= t; -1 behind the last
+// Sequence that owns token t (offsets ascending), by a whole warp; -1: none.
 __device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int64_t t) {
-    if (t < cu[0] || t >= cu[B]) return -1;
-    int lo = 0, hi = B;   // cu[lo] <= t < cu[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cu[mid] <= t) lo = mid;
-        else hi = mid;
+    const int lane = threadIdx.x & 31;
+    int b = -1;   // sequences that start at or before t, minus one
+    for (int b0 = 0; b0 < B; b0 += 32) {
+        const uint32_t m = __ballot_sync(0xffffffffu, b0 + lane < B && cu[b0 + lane] <= t);
+        b += __popc(m);
+        if (m != 0xffffffffu) break;
     }
-    return lo;
+    return b >= 0 && t < cu[b + 1] ? b : -1;
 }
 
-// exponent of a row with largest finite magnitude m: m = f 2^E, f in [1/2, 1), 448 = 0.875 2^9
+// exponent of a row with largest finite magnitude m = f 2^E, f in [1/2, 1): 448 = 0.875 2^9, so that a
+// mantissa above 1.75 needs the next one
 __device__ __forceinline__ int row_exponent(float m) {
-    if (m == 0.f) return 0;
-    int E;
-    const float f = frexpf(m, &E);
-    const int e = f <= 0.875f ? E - 9 : E - 8;
-    return e < -100 ? -100 : e > 119 ? 119 : e;
+    const uint32_t u = __float_as_uint(m);
+    const int e = (int)(u >> 23) - 135 + ((u & 0x7fffffu) > 0x600000u);
+    return m == 0.f ? 0 : e < -100 ? -100 : e > 119 ? 119 : e;
 }
 
-// 8 elements as they are (also the bits of a NaN)
-template <typename T>
-__device__ __forceinline__ void copy8(T* d, const T* s) {
+// 8 elements as floats, and their largest magnitude (bits of a float; infinities and NaN among them stay)
+__device__ __forceinline__ uint32_t open8(const uint4 (&u)[1], float (&x)[8]) {
+    const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(d)[i] = reinterpret_cast<const uint4*>(s)[i];
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+    }
+    return max(m << 16, m & 0xffff0000u);
+}
+__device__ __forceinline__ uint32_t open8(const uint4 (&u)[2], float (&x)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[4 * i + j] = __uint_as_float(w[j]);
+            m = max(m, w[j] & 0x7fffffffu);
+        }
+    }
+    return m;
 }
 
 template <typename T, bool E4M3>
-__global__ void __launch_bounds__(CT) cache_write_kernel(const CacheIo a) {
+__global__ void __launch_bounds__(CT) cache_write_kernel(const __grid_constant__ CacheIo a) {
+    constexpr int W = (int)sizeof(T) / 2, U = 8 / W;   // 16-byte loads of 8 elements, pieces of 8 under way
     const int lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * (CT / 32) + (threadIdx.x >> 5);
     if (t >= a.T) return;
+    const int lph = a.c.D / 8, hpw = 32 / lph, groups = (a.c.H + hpw - 1) / hpw;   // lanes of a head, heads of the warp
+    const int e0 = (lane % lph) * 8, sub = lane / lph;
+    uint4 raw[U][W];
+    auto load = [&](int v0) {   // v: group of heads, keys then values
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int v = v0 + u, side = v >= groups, h = (v - side * groups) * hpw + sub;
+            if (v < 2 * groups && h < a.c.H) {
+                const HeadView& in = side ? a.v : a.k;
+                const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(in.p + t * in.st + h * in.sh) + e0);
+#pragma unroll
+                for (int w = 0; w < W; ++w) raw[u][w] = p[w];
+            } else {
+#pragma unroll
+                for (int w = 0; w < W; ++w) raw[u][w] = make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+    };
+    load(0);
     const int b = sequence_of(a.cu, a.B, t);
     if (b < 0) return;
     const int64_t pos = (int64_t)a.kv_len[b] - (min((int64_t)a.cu[b + 1], a.T) - t);
     if (pos < 0 || pos >= (int64_t)a.c.max_pages * a.c.page_size) return;
-    const HeadView& in = blockIdx.y ? a.v : a.k;
-    char* dst = blockIdx.y ? a.c.v : a.c.k;
-    uint8_t* sc = blockIdx.y ? a.c.vs : a.c.ks;
     const int64_t r0 = cache_row(a.c, b, 0, (int)pos);
     if (r0 < 0) return;
-    const int lph = a.c.D / 8, hpw = 32 / lph;   // 8 elements per lane
-    const int e0 = (lane % lph) * 8;
-    for (int h0 = 0; h0 < a.c.H; h0 += hpw) {
-        const int h = h0 + lane / lph;
-        const bool on = h < a.c.H;
-        const T* src = reinterpret_cast<const T*>(in.p + t * in.st + (on ? h : 0) * in.sh) + e0;
-        const int64_t r = r0 + ((int64_t)h << a.c.page_shift);
-        if (!E4M3) {
-            if (on) copy8(reinterpret_cast<T*>(dst) + r * a.c.D + e0, src);
-            continue;
-        }
-        const float4 x0 = load4f(src), x1 = load4f(src + 4);
-        float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-        float m = 0.f;
+    for (int v0 = 0; v0 < 2 * groups; v0 += U) {
+        if (v0) load(v0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (!isfinite(x[i])) x[i] = __uint_as_float(0x7fc00000u);   // fmaxf drops NaN
-            m = fmaxf(m, fabsf(x[i]));
-        }
-        for (int o = 1; o < lph; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const int e = row_exponent(m);
-        const float inv = pow2i(-e);
-        uint32_t w[2];
+        for (int u = 0; u < U; ++u) {
+            const int v = v0 + u, side = v >= groups, h = (v - side * groups) * hpw + sub;
+            if (v >= 2 * groups) break;
+            const bool on = h < a.c.H;
+            char* dst = side ? a.c.v : a.c.k;
+            const int64_t r = r0 + ((int64_t)h << a.c.page_shift);
+            if (!E4M3) {   // the bits as they are
+                if (on)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i] * inv, x[4 * i + 1] * inv),
-                                                         __NV_SATFINITE, __NV_E4M3);
-            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2] * inv, x[4 * i + 3] * inv),
-                                                         __NV_SATFINITE, __NV_E4M3);
-            w[i] = lo | (hi << 16);
-        }
-        if (on) {
-            *reinterpret_cast<uint2*>(dst + r * a.c.D + e0) = make_uint2(w[0], w[1]);
-            if (e0 == 0) sc[r] = (uint8_t)(e + 127);
+                    for (int w = 0; w < W; ++w) reinterpret_cast<uint4*>(reinterpret_cast<T*>(dst) + r * a.c.D + e0)[w] = raw[u][w];
+                continue;
+            }
+            float x[8];
+            uint32_t mb = open8(raw[u], x);
+            if (__any_sync(0xffffffffu, mb >= 0x7f800000u)) {   // infinities become NaN, and neither counts
+                mb = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (!isfinite(x[i])) x[i] = __uint_as_float(0x7fc00000u);
+                    else mb = max(mb, __float_as_uint(fabsf(x[i])));
+                }
+            }
+            for (int o = 1; o < lph; o <<= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+            const float m = __uint_as_float(mb);
+            const int e = row_exponent(m);
+            const float inv = pow2i(-e);
+            uint32_t w[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i] * inv, x[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+                const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2] * inv, x[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+                w[i] = lo | (hi << 16);
+            }
+            if (on) {
+                *reinterpret_cast<uint2*>(dst + r * a.c.D + e0) = make_uint2(w[0], w[1]);
+                if (e0 == 0) (side ? a.c.vs : a.c.ks)[r] = (uint8_t)(e + 127);
+            }
         }
     }
 }
 
 template <typename TC, typename T>
-__global__ void __launch_bounds__(CT) cache_read_kernel(const CacheIo a) {
+__global__ void __launch_bounds__(CT) cache_read_kernel(const __grid_constant__ CacheIo a) {
+    constexpr bool E8 = sizeof(TC) == 1;
+    constexpr int U = 8, N = 16 / (int)sizeof(T);   // pieces of 16 output bytes under way, elements of one
     const int lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * (CT / 32) + (threadIdx.x >> 5);
     if (t >= a.T) return;
@@ -103,35 +149,54 @@ __global__ void __launch_bounds__(CT) cache_read_kernel(const CacheIo a) {
     if (b < 0) return;
     const int64_t pos = t - max(a.cu[b], 0);
     if (pos >= cache_len(a.c, a.kv_len[b])) return;
-    const HeadView& out = blockIdx.y ? a.v : a.k;
-    const TC* src = reinterpret_cast<const TC*>(blockIdx.y ? a.c.v : a.c.k);
-    const uint8_t* sc = blockIdx.y ? a.c.vs : a.c.ks;
     const int64_t r0 = cache_row(a.c, b, 0, (int)pos);
-    const int lph = a.c.D / 8, hpw = 32 / lph;
-    const int e0 = (lane % lph) * 8;
-    for (int h = lane / lph; h < a.c.H; h += hpw) {
-        T* d = reinterpret_cast<T*>(out.p + t * out.st + h * out.sh) + e0;
-        float4 x0 = make_float4(0.f, 0.f, 0.f, 0.f), x1 = x0;
-        if (r0 >= 0) {
-            const int64_t r = r0 + ((int64_t)h << a.c.page_shift);
-            if constexpr (sizeof(TC) > 1) {
-                copy8(d, src + r * a.c.D + e0);
-                continue;
-            }
-            x0 = load4f(src + r * a.c.D + e0);
-            x1 = load4f(src + r * a.c.D + e0 + 4);
-            if (sizeof(TC) == 1) {
-                const float s = scale_of(sc[r]);
-                x0.x *= s, x0.y *= s, x0.z *= s, x0.w *= s;
-                x1.x *= s, x1.y *= s, x1.z *= s, x1.w *= s;
+    const int lph = a.c.D / N, hpw = 32 / lph, groups = (a.c.H + hpw - 1) / hpw;
+    const int e0 = (lane % lph) * N, sub = lane / lph;
+    for (int v0 = 0; v0 < 2 * groups; v0 += U) {   // groups of heads, keys then values
+        uint4 raw[U];
+        uint8_t sc[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int v = v0 + u, side = v >= groups, h = (v - side * groups) * hpw + sub;
+            raw[u] = make_uint4(0u, 0u, 0u, 0u);
+            sc[u] = 127;
+            if (v < 2 * groups && h < a.c.H && r0 >= 0) {   // no page: zeros
+                const int64_t r = r0 + ((int64_t)h << a.c.page_shift);
+                const TC* src = reinterpret_cast<const TC*>(side ? a.c.v : a.c.k) + r * a.c.D + e0;
+                if constexpr (!E8) raw[u] = *reinterpret_cast<const uint4*>(src);
+                else {
+                    if constexpr (N == 8) {
+                        const uint2 x = *reinterpret_cast<const uint2*>(src);
+                        raw[u].x = x.x, raw[u].y = x.y;
+                    } else raw[u].x = *reinterpret_cast<const uint32_t*>(src);
+                    sc[u] = (side ? a.c.vs : a.c.ks)[r];
+                }
             }
         }
-        store4(d, x0);
-        store4(d + 4, x1);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int v = v0 + u, side = v >= groups, h = (v - side * groups) * hpw + sub;
+            if (v >= 2 * groups || h >= a.c.H) continue;
+            const HeadView& out = side ? a.v : a.k;
+            T* d = reinterpret_cast<T*>(out.p + t * out.st + h * out.sh) + e0;
+            if constexpr (!E8) *reinterpret_cast<uint4*>(d) = raw[u];
+            else {
+                const float s = scale_of(sc[u]);
+                const uint32_t w[2] = {raw[u].x, raw[u].y};
+                float x[N];
+#pragma unroll
+                for (int i = 0; i < N; i += 4) {
+                    const float2 lo = e4m3x2_to_f((uint16_t)w[i / 4]), hi = e4m3x2_to_f((uint16_t)(w[i / 4] >> 16));
+                    x[i] = lo.x * s, x[i + 1] = lo.y * s, x[i + 2] = hi.x * s, x[i + 3] = hi.y * s;
+                }
+                if constexpr (N == 8) *reinterpret_cast<uint4*>(d) = make_uint4(ptx::pack_bf16(x[0], x[1]), ptx::pack_bf16(x[2], x[3]), ptx::pack_bf16(x[4], x[5]), ptx::pack_bf16(x[6], x[7]));
+                else store4(reinterpret_cast<float*>(d), make_float4(x[0], x[1], x[2], x[3]));
+            }
+        }
     }
 }
 
-dim3 token_grid(int64_t T) { return dim3((unsigned)((T + CT / 32 - 1) / (CT / 32)), 2); }
+dim3 token_grid(int64_t T) { return dim3((unsigned)((T + CT / 32 - 1) / (CT / 32))); }
 
 }  // namespace
 

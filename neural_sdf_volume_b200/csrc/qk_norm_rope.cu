@@ -2,35 +2,34 @@
 //
 //   y = x rsqrt(mean(x^2) + eps) gain ; (y_a, y_b) -> m (y_a cos t - y_b sin t, y_a sin t + y_b cos t)
 //
-// One block per token: the token's angles are turned into cos and sin once (float64
-// product pos * inv_freq, reduced to a fraction of a turn in float64, so that a position
-// of a million keeps float32 accuracy; then sincospif) and every head of the token is
-// rotated with them.  A head takes D / VEC lanes of 16 bytes each; a lane's elements and
-// therefore its cos, sin and gains are the same for all heads of its side, so they stay in
-// registers.  The norm is a shuffle sum inside the head's lanes.  Bound by memory: each
-// element is read once and written once.
+// A head takes D / N lanes of 16 bytes each.  One, two or four warps of a block share a token; a
+// lane's elements and therefore its cos and sin are the same for all heads, so they stay in
+// registers.  A lane asks for five heads before it uses the first, and for the first five before
+// the token's angles are turned into cos and sin (float64 product pos * inv_freq, reduced to a
+// fraction of a turn in float64, so that a position of a million keeps float32 accuracy; then
+// sincospif).  The norm is a shuffle sum inside the head's lanes.  Bound by memory: each element is
+// read once and written once.
 #include "seq_internal.cuh"
 
 namespace vdm {
 namespace {
 
 constexpr int RT = 128;   // threads per block
+constexpr int RU = 5;     // heads of a lane in flight
 
 template <typename T> struct Vec;
 template <> struct Vec<float> {
     static constexpr int N = 4;
-    static __device__ __forceinline__ void load(const char* p, float (&x)[4]) {
-        const float4 v = *reinterpret_cast<const float4*>(p);
-        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    static __device__ __forceinline__ void open(uint4 u, float (&x)[4]) {
+        x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y), x[2] = __uint_as_float(u.z), x[3] = __uint_as_float(u.w);
     }
-    static __device__ __forceinline__ void store(char* p, const float (&x)[4]) {
-        *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    static __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
     }
 };
 template <> struct Vec<__nv_bfloat16> {
     static constexpr int N = 8;
-    static __device__ __forceinline__ void load(const char* p, float (&x)[8]) {
-        const uint4 u = *reinterpret_cast<const uint4*>(p);
+    static __device__ __forceinline__ void open(uint4 u, float (&x)[8]) {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -38,112 +37,140 @@ template <> struct Vec<__nv_bfloat16> {
             x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
     }
-    static __device__ __forceinline__ void store(char* p, const float (&x)[8]) {
+    static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
             w[i] = *reinterpret_cast<const uint32_t*>(&b);
         }
-        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
 };
 
-// MODE 0: no rotation, 1: interleaved pairs, 2: halves
+// MODE 0: no rotation, 1: interleaved pairs, 2: halves, 3: halves of a multiple of 4 elements
 template <typename T, int D, int MODE>
-__global__ void __launch_bounds__(RT) qk_norm_rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(RT, 8) qk_norm_rope_kernel(const __grid_constant__ RopeArgs a, const int wpt) {
     constexpr int N = Vec<T>::N, LPH = D / N, HPW = 32 / LPH;
-    __shared__ float s_cos[D / 2], s_sin[D / 2];
-    __shared__ float s_row[RT / 32][HPW][MODE == 2 ? D : 1];
-    const int64_t t = blockIdx.x;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int half = a.rot >> 1;
-    if (MODE != 0) {
-        for (int i = threadIdx.x; i < half; i += RT) {
-            double turns = (double)a.pos[t] * a.inv_freq[i] * 0.15915494309189533577;   // 1 / (2 pi)
-            turns -= rint(turns);
-            float sn, cs;
-            sincospif(2.0f * (float)turns, &sn, &cs);
-            s_cos[i] = cs * a.mscale;
-            s_sin[i] = sn * a.mscale;
-        }
-        __syncthreads();
-    }
+    constexpr int NP = MODE >= 2 ? N : N / 2;   // angles of a lane: of each element, or of each pair
+    __shared__ float s_cos[RT / 32][D / 2], s_sin[RT / 32][D / 2];
+    __shared__ __align__(16) float s_row[RT / 32][HPW][MODE >= 2 ? D : 4];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slot = warp / wpt, part = warp % wpt;
+    const int64_t t = (int64_t)blockIdx.x * (RT / 32 / wpt) + slot;
+    const bool live = t < a.T;
+    const int half = a.rot >> 1, H = a.Hq + a.Hk;
     const int sub = lane / LPH, e0 = (lane % LPH) * N;   // head of the warp's group, first element
-    // element e0 + i: its angle and the sign of its partner's sine
-    float cs[N], sn[N];
-    if (MODE != 0) {
+    uint4 raw[RU];
+    auto load = [&](int h0) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int e = e0 + i;
-            const int pr = MODE == 1 ? e >> 1 : e < half ? e : e - half;
-            const bool first = MODE == 1 ? !(e & 1) : e < half;
+        for (int u = 0; u < RU; ++u) {
+            const int h = h0 + u * wpt * HPW;
+            raw[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (live && h < H) {
+                const char* p = h < a.Hq ? a.q.p + t * a.q.st + h * a.q.sh : a.k.p + t * a.k.st + (h - a.Hq) * a.k.sh;
+                raw[u] = *reinterpret_cast<const uint4*>(p + e0 * (int)sizeof(T));
+            }
+        }
+    };
+    const int first = part * HPW + sub;
+    load(first);
+    float cs[NP], sn[NP];
+    if (MODE != 0) {
+        if (live)
+            for (int i = part * 32 + lane; i < half; i += 32 * wpt) {
+                double turns = (double)a.pos[t] * a.inv_freq[i] * 0.15915494309189533577;   // 1 / (2 pi)
+                turns -= rint(turns);
+                float s, c;
+                sincospif(2.0f * (float)turns, &s, &c);
+                s_cos[slot][i] = c * a.mscale;
+                s_sin[slot][i] = s * a.mscale;
+            }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int e = MODE == 1 ? e0 + 2 * i : e0 + i;
             const bool in = e < a.rot;
-            cs[i] = in ? s_cos[pr] : 1.0f;
-            sn[i] = in ? (first ? -s_sin[pr] : s_sin[pr]) : 0.0f;
+            const int pr = !in ? 0 : MODE == 1 ? e >> 1 : e < half ? e : e - half;
+            cs[i] = in ? s_cos[slot][pr] : 1.0f;
+            sn[i] = in ? s_sin[slot][pr] : 0.0f;
+            if (MODE >= 2 && e < half) sn[i] = -sn[i];   // the first of a pair
         }
     }
+    for (int h0 = first; h0 < H + sub; h0 += RU * wpt * HPW) {   // the same number of rounds for the whole warp
+        if (h0 != first) load(h0);
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-        const int H = side ? a.Hk : a.Hq;
-        const HeadView& in = side ? a.k : a.q;
-        const HeadView& out = side ? a.ko : a.qo;
-        const float* gain = side ? a.gk : a.gq;
-        float g[N];
-        if (gain) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) g[i] = gain[e0 + i];
-        }
-        for (int h0 = warp * HPW; h0 < H; h0 += (RT / 32) * HPW) {
-            const int h = h0 + sub;
+        for (int u = 0; u < RU; ++u) {
+            const int h = h0 + u * wpt * HPW;
+            if (h - sub >= H) break;
             float x[N];
-            if (h < H) Vec<T>::load(in.p + t * in.st + h * in.sh + e0 * sizeof(T), x);
-            else {
+            Vec<T>::open(raw[u], x);
+            const bool isq = h < a.Hq;
+            const float* gain = isq ? a.gq : a.gk;
+            float ss = 0.f;
 #pragma unroll
-                for (int i = 0; i < N; ++i) x[i] = 0.f;
-            }
+            for (int i = 0; i < N; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+            for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
             if (gain) {
-                float ss = 0.f;
-#pragma unroll
-                for (int i = 0; i < N; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-                for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
                 const float r = rsqrtf(ss * (1.0f / D) + a.eps);
 #pragma unroll
-                for (int i = 0; i < N; ++i) x[i] = x[i] * r * g[i];
+                for (int i = 0; i < N; ++i) x[i] = x[i] * r * __ldg(gain + e0 + i);
             }
             if (MODE == 1) {
 #pragma unroll
-                for (int i = 0; i < N; i += 2) {
-                    const float u = x[i], w = x[i + 1];
-                    x[i] = fmaf(u, cs[i], w * sn[i]);
-                    x[i + 1] = fmaf(w, cs[i + 1], u * sn[i + 1]);
+                for (int i = 0; i < N / 2; ++i) {
+                    const float v = x[2 * i], w = x[2 * i + 1];
+                    if (e0 + 2 * i < a.rot) {
+                        x[2 * i] = fmaf(v, cs[i], -(w * sn[i]));
+                        x[2 * i + 1] = fmaf(w, cs[i], v * sn[i]);
+                    }
                 }
-                if (e0 >= a.rot) { /* cs = 1, sn = 0: unchanged */ }
             }
-            if (MODE == 2) {
+            if (MODE >= 2) {
                 float* row = s_row[warp][sub];
 #pragma unroll
-                for (int i = 0; i < N; ++i) row[e0 + i] = x[i];
+                for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(row + e0 + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
                 __syncwarp();
+                if (MODE == 3) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const int e = e0 + i;
-                    if (e < a.rot) x[i] = fmaf(x[i], cs[i], row[e < half ? e + half : e - half] * sn[i]);
+                    for (int i = 0; i < N; i += 4) {
+                        const int e = e0 + i;
+                        if (e < a.rot) {
+                            const float4 y = *reinterpret_cast<const float4*>(row + (e < half ? e + half : e - half));
+                            x[i] = fmaf(x[i], cs[i], y.x * sn[i]);
+                            x[i + 1] = fmaf(x[i + 1], cs[i + 1], y.y * sn[i + 1]);
+                            x[i + 2] = fmaf(x[i + 2], cs[i + 2], y.z * sn[i + 2]);
+                            x[i + 3] = fmaf(x[i + 3], cs[i + 3], y.w * sn[i + 3]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        const int e = e0 + i;
+                        if (e < a.rot) x[i] = fmaf(x[i], cs[i], row[e < half ? e + half : e - half] * sn[i]);
+                    }
                 }
                 __syncwarp();
             }
-            if (h < H) Vec<T>::store(out.p + t * out.st + h * out.sh + e0 * sizeof(T), x);
+            if (live && h < H) {
+                char* p = isq ? a.qo.p + t * a.qo.st + h * a.qo.sh : a.ko.p + t * a.ko.st + (h - a.Hq) * a.ko.sh;
+                *reinterpret_cast<uint4*>(p + e0 * (int)sizeof(T)) = Vec<T>::pack(x);
+            }
         }
     }
 }
 
 template <typename T, int D>
 void launch(const RopeArgs& a, cudaStream_t s) {
-    const dim3 grid((unsigned)a.T);
-    if (!a.rot) qk_norm_rope_kernel<T, D, 0><<<grid, RT, 0, s>>>(a);
-    else if (a.interleaved) qk_norm_rope_kernel<T, D, 1><<<grid, RT, 0, s>>>(a);
-    else qk_norm_rope_kernel<T, D, 2><<<grid, RT, 0, s>>>(a);
+    // warps of a token: as many as its heads keep busy; all four where tokens are few
+    const int vecs = (a.Hq + a.Hk) * (D / Vec<T>::N);
+    const int wpt = a.T <= 592 || vecs >= 4 * 32 * RU ? 4 : vecs >= 2 * 32 * RU ? 2 : 1;
+    const int64_t per = RT / 32 / wpt;
+    const dim3 grid((unsigned)((a.T + per - 1) / per));
+    if (!a.rot) qk_norm_rope_kernel<T, D, 0><<<grid, RT, 0, s>>>(a, wpt);
+    else if (a.interleaved) qk_norm_rope_kernel<T, D, 1><<<grid, RT, 0, s>>>(a, wpt);
+    else if (a.rot % 8 == 0) qk_norm_rope_kernel<T, D, 3><<<grid, RT, 0, s>>>(a, wpt);
+    else qk_norm_rope_kernel<T, D, 2><<<grid, RT, 0, s>>>(a, wpt);
 }
 
 }  // namespace

@@ -1,6 +1,8 @@
 // Host side of the token-sequence operators declared in include/vdm.h: argument checks,
 // workspace layout, choice of the kernel.
 #include <math.h>
+#include <stdio.h>
+#include <stdlib.h>
 #include <string.h>
 
 #include <atomic>
@@ -112,40 +114,60 @@ vdm_status check_attention(const vdm_attention* a) {
 
 // Kernel and number of blocks that share a row tile's keys.  Depends on sizes alone, so that
 // the workspace can be asked for beforehand.
-enum Kernel : int { kSimt, kTc, kRows };
+enum Kernel : int { kSimt, kTc, kRows, kRowsF32 };
 struct Plan {
     int kernel, splits, cluster;
 };
 
 Plan plan_attention(const vdm_attention* at, int B, int64_t Tq, int64_t max_kv) {
     Plan p;
-    const int64_t G = at->Hq / at->Hk, seqs = B < Tq ? B : Tq;
     p.splits = p.cluster = 1;
-    p.kernel = at->dtype == VDM_F32 ? kSimt : kTc;
+    const bool bf16 = at->dtype != VDM_F32;
+    p.kernel = bf16 ? kTc : kSimt;
+    const int64_t G = at->Hq / at->Hk, seqs = B < Tq ? B : Tq;
     if (seqs == 0) return p;
-    if (p.kernel == kTc && Tq * G <= 32 * seqs) {
-        p.kernel = kRows;
-        const int64_t M = rows_tile((int)G, Tq, B), tiles = (Tq * G + seqs * (M - 1)) / M * at->Hk;
-        const int64_t steps = (max_kv + 31) / 32;
-        while (p.cluster < 16 && tiles * p.cluster < 1500 && p.cluster * 4 <= steps) p.cluster *= 2;
-        if (p.cluster == 16)
-            while (p.splits < 16 && tiles * p.cluster * p.splits < 296 && p.splits * p.cluster * 32 < steps) p.splits *= 2;
-        return p;
-    }
-    // Row tiles of the kernel, blocks that run at once, and the cost of a block in steps of N keys: its
-    // own share of the keys, and a start and end that take as long as four steps.  Joining s parts writes
-    // and reads s rows of floats, at 9 MB a step.  The number of splits is the one with the shortest sum.
-    const int64_t M = p.kernel == kTc ? tc_rows(at->D) : 64, N = p.kernel == kTc ? 128 : 64, at_once = p.kernel == kTc ? 148 * tc_per_sm(at->D) : 296;
-    const int64_t tiles = (Tq * G + seqs * (M - 1)) / M * at->Hk, nk = (max_kv + N - 1) / N;
+    // Keys of a sequence and share of them that a query sees: as many keys as queries in all are taken for
+    // packed self-attention with sequences of up to twice the average.
+    const bool self = max_kv == Tq && Tq > seqs;
+    const double kv = self ? (double)max_kv * 2.0 / seqs < (double)max_kv ? (double)max_kv * 2.0 / seqs : (double)max_kv : (double)max_kv;
+    const double share = self && at->causal ? 0.5 : 1.0;
+
+    // Row tiles of the large-tile kernels, blocks that run at once, and the cost of a block in steps of N
+    // keys: its own share of the keys, and a start and end that take as long as four steps.  With many
+    // blocks the longest half overlaps the others; joining s parts writes and reads s rows of floats,
+    // at 9 MB a step.  The number of splits is the one with the shortest sum.
+    const int64_t M = bf16 ? tc_rows(at->D) : 64, N = bf16 ? 128 : 64, at_once = bf16 ? 148 * tc_per_sm(at->D) : 296;
+    const int64_t tiles = (Tq * G + seqs * (M - 1)) / M * at->Hk;
+    const double nk = ceil(kv / N);
     double best = 0;
     for (int s = 1; s <= 64 && s * 2 <= (nk > 2 ? nk : 2); ++s) {
-        const double waves = (double)((tiles * s + at_once - 1) / at_once);
-        const double cost = waves * ((double)((nk + s - 1) / s) + 4.0) + (s > 1 ? 2.0 + s * (double)(Tq * at->Hq * at->D * 8) / 9e6 : 0.0);
+        const double mine = ceil(nk / s) + 4.0, all = (double)tiles * s * (ceil(nk / s) * share + 4.0) / at_once;
+        const double cost = (tiles * s <= at_once ? mine : all + 0.5 * mine > mine ? all + 0.5 * mine : mine) +
+                            (s > 1 ? 2.0 + s * (double)(Tq * at->Hq * at->D * 8) / 9e6 : 0.0);
         if (s == 1 || cost < 0.95 * best) {
             best = cost;
             p.splits = s;
         }
     }
+    // The few-row kernels: tiles of R rows, keys shared by the four warps of each of up to eight blocks.
+    const int64_t R = bf16 ? rows_tile((int)G, Tq, B) : rows_tile_f32((int)G, Tq, B);
+    const int64_t few = (Tq * G + seqs * (R - 1)) / R * at->Hk, steps = (int64_t)(kv + 31) / 32;
+    // Time of either, us: a few-row block's start and end take 4, a warp's step of 32 keys with 12 warps on an
+    // SM 6 (16 rows, D = 128), about half of that with 8 rows or D = 64, and alone at least 1; a large-tile
+    // step takes 1.85 (1.5 at D = 64).
+    const double step = (at->D == 64 ? 3.6 : 6.0) * (bf16 && R == 8 ? 0.6 : 1.0), t_large = best * (at->D == 64 ? 1.5 : 1.85);
+    const double t_few = 4.0 + (double)few * steps * share * step / (148 * 12);
+    if (bf16 ? t_few < t_large : Tq * G <= 64 * seqs) {
+        p.kernel = bf16 ? kRows : kRowsF32;
+        p.splits = 1;
+        // Blocks of a tile: until three are on every SM and a warp has half a step, or, for the sake of ragged
+        // lengths, until there are some 1500 with at least 16 steps a warp.
+        while (p.cluster < 8 && ((few * p.cluster < 444 && p.cluster * 4 <= steps) || (few * p.cluster < 1500 && p.cluster * 128 <= steps)))
+            p.cluster *= 2;
+        if (p.cluster == 8)
+            while (p.splits < 16 && few * 8 * p.splits < 296 && p.splits * 192 <= steps) p.splits *= 2;
+    }
+    if (const char* e = getenv("VDM_DEV_K")) { int k, c, sp; sscanf(e, "%d,%d,%d", &k, &c, &sp); if (k >= 0) p.kernel = k; if (c > 0) p.cluster = c; if (sp > 0) p.splits = sp; }
     return p;
 }
 
@@ -177,6 +199,7 @@ vdm_status run_attention(const vdm_attention* at, AttnArgs& a, int64_t max_kv, c
     a.timeout = 4000000000ll;   // cycles of one bounded wait, about two seconds
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (plan.kernel == kRows) return launch_attention_rows(a, st);
+    if (plan.kernel == kRowsF32) return launch_attention_rows_f32(a, st);
     return plan.kernel == kTc ? launch_attention_tc(a, st) : launch_attention_simt(a, at->dtype, st);
 }
 

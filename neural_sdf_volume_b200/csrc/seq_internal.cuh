@@ -245,25 +245,29 @@ __device__ __forceinline__ float repair_row(const AttnArgs& a, const RowTile& t,
 
 // rows of a tile of the few-rows kernel
 inline int rows_tile(int G, int64_t Tq, int B) { return Tq * G <= 8 * (B < Tq ? B : Tq) ? 8 : 16; }
+inline int rows_tile_f32(int G, int64_t Tq, int B) {
+    const int64_t n = B < Tq ? B : Tq, rows = Tq * G;
+    return rows <= n ? 1 : rows <= 2 * n ? 2 : 4;
+}
 
 // query rows of a block of the tensor-core kernel, and such blocks on an SM
 __host__ __device__ constexpr int tc_rows(int D) { return D == 64 ? 128 : 256; }
 constexpr int tc_per_sm(int D) { return D == 64 ? 2 : 1; }
 
-// Shared memory size (and clusters of 16 blocks) of a kernel, set once per device.
-inline vdm_status prepare_kernel(std::atomic<uint64_t>& ready, const void* f, int smem, bool clusters = false) {
+// Shared memory size of a kernel, set once per device.
+inline vdm_status prepare_kernel(std::atomic<uint64_t>& ready, const void* f, int smem) {
     int dev = 0;
     VDM_CUDA_TRY(cudaGetDevice(&dev));
     const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
     if (ready.load() & bit) return VDM_OK;
-    VDM_CUDA_TRY(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    if (clusters) VDM_CUDA_TRY(cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+    if (smem) VDM_CUDA_TRY(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     ready.fetch_or(bit);
     return VDM_OK;
 }
 
 // launchers
 vdm_status launch_attention_rows(const AttnArgs& a, cudaStream_t s);
+vdm_status launch_attention_rows_f32(const AttnArgs& a, cudaStream_t s);
 vdm_status launch_attention_simt(const AttnArgs& a, vdm_dtype dt, cudaStream_t s);
 vdm_status launch_attention_tc(const AttnArgs& a, cudaStream_t s);
 vdm_status launch_combine(const AttnArgs& a, vdm_dtype dt, cudaStream_t s);
