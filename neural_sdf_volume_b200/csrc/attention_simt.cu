@@ -8,25 +8,34 @@
 // keys tx + 16 j of the scores, and columns 4 tx + 64 j of the output: 128 fused multiply-adds
 // for twelve 16-byte shared loads, eight of them the same for half a warp.  Bound by the FMA pipe.
 //
+// Float32 tiles come by asynchronous copies: the next keys while this tile's softmax and product
+// with the values run, the next values during the next scores.
+//
 // A key that a row does not see has score -inf and weight 0; since 0 * NaN would still reach
-// the row through the product with v, a value row that not every row of the tile may see is
-// multiplied only where the weight is the row's own (see MASKED).
+// the row through the product with v, a tile whose rows see different numbers of keys multiplies
+// a value only where the row sees it.
 #include "seq_internal.cuh"
+#include "tc_ptx.cuh"
+
+#include <type_traits>
 
 namespace vdm {
 namespace {
 
-constexpr int BR = 64, BK = 64, ST = 128, TR = 8;   // TR: rows of a thread
+constexpr int BR = 64, ST = 128, TR = 8;   // rows of a tile, threads, rows of a thread
 constexpr float kLn2 = 0.69314718055994530942f;
 
+constexpr int simt_smem(int D) { return ((BR + 2 * simt_keys(D)) * (D + 4) + BR * (simt_keys(D) + 4)) * 4; }
+
 template <typename T, typename TC, int D, bool PAGED>
-__global__ void __launch_bounds__(ST, D == 64 ? 3 : 2) attention_simt_kernel(const AttnArgs a) {
-    constexpr int LD = D + 4, LP = BK + 4, NC = D / 64;
+__global__ void __launch_bounds__(ST, D == 64 ? 3 : 2) attention_simt_kernel(const __grid_constant__ AttnArgs a) {
+    constexpr int BK = simt_keys(D), LD = D + 4, LP = BK + 4, NC = D / 64, TK = BK / 16;
+    constexpr bool COPY = sizeof(TC) == 4;   // as they are
     extern __shared__ float4 smem4[];
     float* Qs = reinterpret_cast<float*>(smem4);
     float* Ks = Qs + BR * LD;
     float* Vs = Ks + BK * LD;
-    float* Ps = Ks;   // the weights replace the keys once every score of the tile is computed
+    float* Ps = Vs + BK * LD;
     RowTile t;
     if (!find_tile(a, blockIdx.x, BR, a.causal, t)) return;
     const int hk = blockIdx.y, split = blockIdx.z;
@@ -34,6 +43,7 @@ __global__ void __launch_bounds__(ST, D == 64 ? 3 : 2) attention_simt_kernel(con
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int n_rows = min(BR, (int)((int64_t)t.nq * a.G - t.row0));
 
+#pragma unroll 8
     for (int i = tid; i < BR * (D / 4); i += ST) {
         const int r = i / (D / 4), d = (i % (D / 4)) * 4;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -61,30 +71,53 @@ __global__ void __launch_bounds__(ST, D == 64 ? 3 : 2) attention_simt_kernel(con
     const int most = keys_seen(a, t, (t.row0 + n_rows - 1) / a.G), least = keys_seen(a, t, t.row0 / a.G);
     const int n_tiles = (most + BK - 1) / BK, per = (n_tiles + a.splits - 1) / a.splits;
     const int j_end = min(most, (split + 1) * per * BK);
-    for (int j0 = split * per * BK; j0 < j_end; j0 += BK) {
-        __syncthreads();
-        for (int i = tid; i < BK * (D / 4); i += ST) {
-            const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-            if (j0 + r < most) {
-                x = kv.get(false, j0 + r, d);
-                y = kv.get(true, j0 + r, d);
+    // a tile of keys or values into shared memory; rows from `most` on are zeros
+    auto fetch = [&](bool value, int j0) {
+        float* dst = value ? Vs : Ks;
+        if (COPY) {
+#pragma unroll
+            for (int i = 0; i < BK * (D / 4) / ST; ++i) {
+                const int x = tid + ST * i, r = x / (D / 4), d = (x % (D / 4)) * 4, key = j0 + r;
+                const char* src = nullptr;
+                if (key < most) {
+                    if (PAGED) {
+                        const int64_t row = cache_row(a.c, t.b, hk, key);
+                        if (row >= 0) src = (value ? a.c.v : a.c.k) + (row * D + d) * 4;
+                    } else {
+                        const HeadView& h = value ? a.v : a.k;
+                        src = h.p + (t.k0 + key) * h.st + hk * h.sh + d * 4;
+                    }
+                }
+                ptx::cp_async16(ptx::smem_u32(dst + r * LD + d), src ? src : a.q.p, src != nullptr);
             }
-            *reinterpret_cast<float4*>(Ks + r * LD + d) = x;
-            *reinterpret_cast<float4*>(Vs + r * LD + d) = y;
+        } else {
+#pragma unroll 8
+            for (int i = 0; i < BK * (D / 4) / ST; ++i) {
+                const int x = tid + ST * i, r = x / (D / 4), d = (x % (D / 4)) * 4;
+                *reinterpret_cast<float4*>(dst + r * LD + d) = j0 + r < most ? kv.get(value, j0 + r, d) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
         }
+        ptx::cp_async_commit();
+    };
+    const int j_begin = split * per * BK;
+    if (j_begin < j_end) {
+        fetch(false, j_begin);
+        fetch(true, j_begin);
+    }
+    for (int j0 = j_begin; j0 < j_end; j0 += BK) {
+        ptx::cp_async_wait<1>();   // the keys are there
         __syncthreads();
-        float s[TR][4] = {};
+        float s[TR][TK] = {};
 #pragma unroll 2
         for (int d = 0; d < D; d += 4) {
-            float4 kk[4];
+            float4 kk[TK];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) kk[j] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * j) * LD + d);
+            for (int j = 0; j < TK; ++j) kk[j] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * j) * LD + d);
 #pragma unroll
             for (int i = 0; i < TR; ++i) {
                 const float4 qv = *reinterpret_cast<const float4*>(Qs + (TR * ty + i) * LD + d);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < TK; ++j) {
                     s[i][j] = fmaf(qv.x, kk[j].x, s[i][j]);
                     s[i][j] = fmaf(qv.y, kk[j].y, s[i][j]);
                     s[i][j] = fmaf(qv.z, kk[j].z, s[i][j]);
@@ -93,11 +126,13 @@ __global__ void __launch_bounds__(ST, D == 64 ? 3 : 2) attention_simt_kernel(con
             }
         }
         __syncthreads();
+        if (j0 + BK < j_end) fetch(false, j0 + BK);
+        else ptx::cp_async_commit();
 #pragma unroll
         for (int i = 0; i < TR; ++i) {
             float mx = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < TK; ++j) {
                 s[i][j] = j0 + tx + 16 * j < seen[i] ? s[i][j] * a.scale_log2 : -INFINITY;
                 mx = fmaxf(mx, s[i][j]);
             }
@@ -107,7 +142,7 @@ __global__ void __launch_bounds__(ST, D == 64 ? 3 : 2) attention_simt_kernel(con
             const float f = exp2f(m[i] - base);
             float sum = 0.f;   // of this thread's keys; the row's at the end
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < TK; ++j) {
                 const float p = exp2f(s[i][j] - base);
                 sum += p;
                 Ps[(TR * ty + i) * LP + tx + 16 * j] = p;
@@ -119,35 +154,41 @@ __global__ void __launch_bounds__(ST, D == 64 ? 3 : 2) attention_simt_kernel(con
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[i][c][e] *= f;
         }
-        __syncwarp();   // a row's weights are written and read by the same half-warp
-        // MASKED: rows of the tile see different numbers of keys; then a value row counts only
-        // for rows that see it
-        const bool masked = j0 + BK > least;
+        ptx::cp_async_wait<1>();   // the values are there
+        __syncthreads();
+        auto product = [&](auto masked) {
 #pragma unroll 2
-        for (int j = 0; j < BK; j += 4) {
-            float4 v[4][NC];
+            for (int j = 0; j < BK; j += 4) {
+                float4 v[4][NC];
 #pragma unroll
-            for (int jj = 0; jj < 4; ++jj)
+                for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
-                for (int c = 0; c < NC; ++c) v[jj][c] = *reinterpret_cast<const float4*>(Vs + (j + jj) * LD + 64 * c + 4 * tx);
+                    for (int c = 0; c < NC; ++c) v[jj][c] = *reinterpret_cast<const float4*>(Vs + (j + jj) * LD + 64 * c + 4 * tx);
 #pragma unroll
-            for (int i = 0; i < TR; ++i) {
-                const float4 p = *reinterpret_cast<const float4*>(Ps + (TR * ty + i) * LP + j);
+                for (int i = 0; i < TR; ++i) {
+                    const float4 p = *reinterpret_cast<const float4*>(Ps + (TR * ty + i) * LP + j);
 #pragma unroll
-                for (int jj = 0; jj < 4; ++jj) {
-                    const float w = jj == 0 ? p.x : jj == 1 ? p.y : jj == 2 ? p.z : p.w;
-                    if (masked && j0 + j + jj >= seen[i]) continue;
+                    for (int jj = 0; jj < 4; ++jj) {
+                        const float w = jj == 0 ? p.x : jj == 1 ? p.y : jj == 2 ? p.z : p.w;
+                        if (decltype(masked)::value && j0 + j + jj >= seen[i]) continue;
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) {
-                        o[i][c][0] = fmaf(w, v[jj][c].x, o[i][c][0]);
-                        o[i][c][1] = fmaf(w, v[jj][c].y, o[i][c][1]);
-                        o[i][c][2] = fmaf(w, v[jj][c].z, o[i][c][2]);
-                        o[i][c][3] = fmaf(w, v[jj][c].w, o[i][c][3]);
+                        for (int c = 0; c < NC; ++c) {
+                            o[i][c][0] = fmaf(w, v[jj][c].x, o[i][c][0]);
+                            o[i][c][1] = fmaf(w, v[jj][c].y, o[i][c][1]);
+                            o[i][c][2] = fmaf(w, v[jj][c].z, o[i][c][2]);
+                            o[i][c][3] = fmaf(w, v[jj][c].w, o[i][c][3]);
+                        }
                     }
                 }
             }
-        }
+        };
+        if (j0 + BK > least) product(std::true_type{});
+        else product(std::false_type{});
+        __syncthreads();
+        if (j0 + BK < j_end) fetch(true, j0 + BK);
+        else ptx::cp_async_commit();
     }
+    ptx::cp_async_wait<0>();
 #pragma unroll
     for (int i = 0; i < TR; ++i)
 #pragma unroll
@@ -208,10 +249,10 @@ __global__ void __launch_bounds__(128) combine_kernel(const AttnArgs a) {
 
 template <typename T, typename TC, int D, bool PAGED>
 vdm_status launch(const AttnArgs& a, cudaStream_t s) {
-    const size_t smem = (size_t)3 * 64 * (D + 4) * 4;
+    const int smem = simt_smem(D);
     auto kern = attention_simt_kernel<T, TC, D, PAGED>;
     static std::atomic<uint64_t> ready{0};
-    VDM_TRY(prepare_kernel(ready, reinterpret_cast<const void*>(kern), (int)smem));
+    VDM_TRY(prepare_kernel(ready, reinterpret_cast<const void*>(kern), smem));
     const int64_t tiles = (a.Tq * a.G + (a.B < a.Tq ? a.B : a.Tq) * (int64_t)(BR - 1)) / BR;
     kern<<<dim3((unsigned)tiles, a.Hk, a.splits), ST, smem, s>>>(a);
     VDM_TRY(check_launch("attention_simt_kernel"));

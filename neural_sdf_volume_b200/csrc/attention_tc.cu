@@ -537,26 +537,36 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         }
     } else {
         // ------------------------------------------------------------ 8-bit tiles widened to bf16
-        constexpr int CT = 32 * C::WIDEN;
-        const int ct = tid - 32 * (MMA_WARP + 1);
-        for (int it = 0; it < 2 * (jmax - jb); ++it) {
-            const int slot = it % NS, j0 = (jb + (it >> 1)) * BN;
-            if (it >= NS && !wait(&sh.empty[slot], ((it / NS) - 1) & 1, 9)) break;
-            const char* src = it & 1 ? a.c.v : a.c.k;
-            const uint8_t* sc = it & 1 ? a.c.vs : a.c.ks;
-            const uint32_t dst = s_ring + slot * C::SLOT;
-            constexpr int CH = D / 16;   // 16-code chunks of a row
-#pragma unroll 4
-            for (int x = ct; x < BN * CH; x += CT) {
-                const int r = x / CH, c = x % CH;
-                const int64_t row = j0 + r < t.nk ? cache_row(a.c, t.b, hk, j0 + r) : -1;
-                uint4 u = make_uint4(0u, 0u, 0u, 0u);
-                float f = 0.f;
+        // A thread keeps one column of 16 codes and every ROWS-th row of a tile; a row of the next tile is asked
+        // for as soon as this tile's is widened.
+        constexpr int CH = D / 16, ROWS = 32 * C::WIDEN / CH, U = (BN + ROWS - 1) / ROWS;
+        const int ct = tid - 32 * (MMA_WARP + 1), c = ct % CH, r0 = ct / CH;
+        const int items = 2 * (jmax - jb);
+        uint4 code[U];
+        uint32_t scale[U];
+        auto ask = [&](int it, int u) {
+            const int r = r0 + u * ROWS, key = (jb + (it >> 1)) * BN + r;
+            code[u] = make_uint4(0u, 0u, 0u, 0u);
+            scale[u] = 127;
+            if (it < items && r < BN && key < t.nk) {
+                const int64_t row = cache_row(a.c, t.b, hk, key);
                 if (row >= 0) {
-                    u = *reinterpret_cast<const uint4*>(src + row * D + c * 16);
-                    f = scale_of(sc[row]);
+                    code[u] = *reinterpret_cast<const uint4*>((it & 1 ? a.c.v : a.c.k) + row * D + c * 16);
+                    scale[u] = (it & 1 ? a.c.vs : a.c.ks)[row];
                 }
-                const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+            }
+        };
+#pragma unroll
+        for (int u = 0; u < U; ++u) ask(0, u);
+        for (int it = 0; it < items; ++it) {
+            const int slot = it % NS;
+            if (it >= NS && !wait(&sh.empty[slot], ((it / NS) - 1) & 1, 9)) break;
+            const uint32_t dst = s_ring + slot * C::SLOT;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int r = r0 + u * ROWS;
+                const float f = scale_of((uint8_t)scale[u]);
+                const uint32_t in[4] = {code[u].x, code[u].y, code[u].z, code[u].w};
                 uint32_t o[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -564,8 +574,11 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     o[2 * i] = pack_bf16(lo.x * f, lo.y * f);
                     o[2 * i + 1] = pack_bf16(hi.x * f, hi.y * f);
                 }
-                st_v4(dst + tile_off(r, 2 * c), o[0], o[1], o[2], o[3]);
-                st_v4(dst + tile_off(r, 2 * c + 1), o[4], o[5], o[6], o[7]);
+                if (r < BN) {
+                    st_v4(dst + tile_off(r, 2 * c), o[0], o[1], o[2], o[3]);
+                    st_v4(dst + tile_off(r, 2 * c + 1), o[4], o[5], o[6], o[7]);
+                }
+                ask(it + 1, u);
             }
             fence_proxy_async();
             warp_arrive(&sh.full[slot]);

@@ -1,8 +1,6 @@
 // Host side of the token-sequence operators declared in include/vdm.h: argument checks,
 // workspace layout, choice of the kernel.
 #include <math.h>
-#include <stdio.h>
-#include <stdlib.h>
 #include <string.h>
 
 #include <atomic>
@@ -132,42 +130,42 @@ Plan plan_attention(const vdm_attention* at, int B, int64_t Tq, int64_t max_kv) 
     const double kv = self ? (double)max_kv * 2.0 / seqs < (double)max_kv ? (double)max_kv * 2.0 / seqs : (double)max_kv : (double)max_kv;
     const double share = self && at->causal ? 0.5 : 1.0;
 
-    // Row tiles of the large-tile kernels, blocks that run at once, and the cost of a block in steps of N
-    // keys: its own share of the keys, and a start and end that take as long as four steps.  With many
-    // blocks the longest half overlaps the others; joining s parts writes and reads s rows of floats,
-    // at 9 MB a step.  The number of splits is the one with the shortest sum.
-    const int64_t M = bf16 ? tc_rows(at->D) : 64, N = bf16 ? 128 : 64, at_once = bf16 ? 148 * tc_per_sm(at->D) : 296;
+    // Large-tile kernels: row tiles, blocks that run at once, and the cost of a block in steps of N keys: its
+    // own share of the keys, and its start and end.  With many blocks the longest half overlaps the others.
+    // Joining s parts takes a launch, and s rows of floats written and read at 5 TB/s.  The number of splits is
+    // the one with the shortest sum.  Measured, us: a step 1.85 and a start and end 7.4 (tensor cores, D = 128),
+    // 1.5 and 6 (D = 64); 7 and 7 (CUDA cores).
+    const int64_t M = bf16 ? tc_rows(at->D) : 64, N = bf16 ? 128 : simt_keys(at->D), at_once = bf16 ? 148 * tc_per_sm(at->D) : 296;
+    const double step = !bf16 ? 7.0 : at->D == 64 ? 1.5 : 1.85, ends = bf16 ? 4.0 * step : step;
     const int64_t tiles = (Tq * G + seqs * (M - 1)) / M * at->Hk;
     const double nk = ceil(kv / N);
     double best = 0;
     for (int s = 1; s <= 64 && s * 2 <= (nk > 2 ? nk : 2); ++s) {
-        const double mine = ceil(nk / s) + 4.0, all = (double)tiles * s * (ceil(nk / s) * share + 4.0) / at_once;
+        const double part = ceil(nk / s) * step, mine = part + ends, all = (double)tiles * s * (part * share + ends) / at_once;
         const double cost = (tiles * s <= at_once ? mine : all + 0.5 * mine > mine ? all + 0.5 * mine : mine) +
-                            (s > 1 ? 2.0 + s * (double)(Tq * at->Hq * at->D * 8) / 9e6 : 0.0);
+                            (s > 1 ? 3.5 + s * (double)(Tq * at->Hq * at->D * 8) / 5e6 : 0.0);
         if (s == 1 || cost < 0.95 * best) {
             best = cost;
             p.splits = s;
         }
     }
     // The few-row kernels: tiles of R rows, keys shared by the four warps of each of up to eight blocks.
+    // Measured, us: a block's start and end 4; a warp's step of 32 keys with 12 warps on an SM 6 (16 rows, D =
+    // 128) and 3.6 (D = 64), with 8 rows 0.6 of that; float32 10 and 5.6 (4 rows).
     const int64_t R = bf16 ? rows_tile((int)G, Tq, B) : rows_tile_f32((int)G, Tq, B);
-    const int64_t few = (Tq * G + seqs * (R - 1)) / R * at->Hk, steps = (int64_t)(kv + 31) / 32;
-    // Time of either, us: a few-row block's start and end take 4, a warp's step of 32 keys with 12 warps on an
-    // SM 6 (16 rows, D = 128), about half of that with 8 rows or D = 64, and alone at least 1; a large-tile
-    // step takes 1.85 (1.5 at D = 64).
-    const double step = (at->D == 64 ? 3.6 : 6.0) * (bf16 && R == 8 ? 0.6 : 1.0), t_large = best * (at->D == 64 ? 1.5 : 1.85);
-    const double t_few = 4.0 + (double)few * steps * share * step / (148 * 12);
-    if (bf16 ? t_few < t_large : Tq * G <= 64 * seqs) {
+    const int64_t few = seqs * (((Tq * G + seqs - 1) / seqs + R - 1) / R) * at->Hk, steps = (int64_t)(kv + 31) / 32;
+    const double few_step = (at->D == 64 ? (bf16 ? 3.6 : 5.6) : bf16 ? 6.0 : 10.0) * (R == 8 ? 0.6 : R < 4 ? 0.25 * R : 1.0);
+    if (4.0 + (double)few * steps * share * few_step / (148 * 12) < best) {
         p.kernel = bf16 ? kRows : kRowsF32;
         p.splits = 1;
-        // Blocks of a tile: until three are on every SM and a warp has half a step, or, for the sake of ragged
+        // Blocks of a tile: until the SMs are full and a warp has half a step, or, for the sake of ragged
         // lengths, until there are some 1500 with at least 16 steps a warp.
-        while (p.cluster < 8 && ((few * p.cluster < 444 && p.cluster * 4 <= steps) || (few * p.cluster < 1500 && p.cluster * 128 <= steps)))
+        const int64_t full = bf16 || at->D == 64 ? 444 : 222;
+        while (p.cluster < 8 && ((few * p.cluster < full && p.cluster * 4 <= steps) || (few * p.cluster < 1500 && p.cluster * 128 <= steps)))
             p.cluster *= 2;
         if (p.cluster == 8)
             while (p.splits < 16 && few * 8 * p.splits < 296 && p.splits * 192 <= steps) p.splits *= 2;
     }
-    if (const char* e = getenv("VDM_DEV_K")) { int k, c, sp; sscanf(e, "%d,%d,%d", &k, &c, &sp); if (k >= 0) p.kernel = k; if (c > 0) p.cluster = c; if (sp > 0) p.splits = sp; }
     return p;
 }
 

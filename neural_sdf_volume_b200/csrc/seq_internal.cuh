@@ -250,6 +250,8 @@ inline int rows_tile_f32(int G, int64_t Tq, int B) {
     return rows <= n ? 1 : rows <= 2 * n ? 2 : 4;
 }
 
+// keys of a tile of the CUDA-core kernel: a block's Q, K, V and weights fit an SM three times (D = 64) or twice
+__host__ __device__ constexpr int simt_keys(int D) { return D == 64 ? 64 : 32; }
 // query rows of a block of the tensor-core kernel, and such blocks on an SM
 __host__ __device__ constexpr int tc_rows(int D) { return D == 64 ? 128 : 256; }
 constexpr int tc_per_sm(int D) { return D == 64 ? 2 : 1; }
