@@ -27,8 +27,8 @@
 // bf16 values: e = 0 and w is rounded to bf16.
 // The reference follows the maximum when that has grown by more than 2^3.
 //
-// Masked keys: rows of V behind the sequence's end are read as zeros.  Rows inside it that
-// only later queries of the tile see can bring 0 * NaN; see repair_row.
+// Masked keys: rows of V that no row of the tile sees are read as zeros.  Rows that
+// only its later queries see can bring 0 * NaN; see repair_row.
 #include <type_traits>
 
 #include "attention_join.cuh"
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(RW * 32, 3) attention_rows_kernel(const __grid
         for (int u = 0; u < U; ++u) {
             pg[u] = -1;
             const int pos = step * KS + 16 * u;
-            if (PAGED && step < s1 && pos < t.nk) pg[u] = a.c.table[(int64_t)t.b * a.c.max_pages + (pos >> a.c.page_shift)];
+            if (PAGED && step < s1 && pos < most) pg[u] = a.c.table[(int64_t)t.b * a.c.max_pages + (pos >> a.c.page_shift)];
         }
     };
     auto issue = [&](int step, int slot, const int (&pg)[U]) {
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(RW * 32, 3) attention_rows_kernel(const __grid
                     sk = a.k.p + (t.k0 + pos0) * a.k.st + hk * a.k.sh;
                     sv = a.v.p + (t.k0 + pos0) * a.v.st + hk * a.v.sh;
                 }
-                if (on && pos0 + 16 <= t.nk) {
+                if (on && pos0 + 16 <= most) {
 #pragma unroll
                     for (int i = 0; i < CH / 2; ++i) {
                         const int x = lane + 32 * i, r = x / CH, c = x % CH;
@@ -162,11 +162,11 @@ __global__ void __launch_bounds__(RW * 32, 3) attention_rows_kernel(const __grid
                         cp16(dv + (16 * u + r) * RB + swizzle_v<CH>(r, c) * 16, sv + r * (PAGED ? RB : a.v.st) + c * 16, true);
                     }
                 } else {
-                    // no page, or the sequence ends here: zeros (nothing is read, the address stays inside the tensors)
+                    // no page, or no row of the tile sees more: zeros (nothing is read, the address stays inside the tensors)
 #pragma unroll
                     for (int i = 0; i < CH / 2; ++i) {
                         const int x = lane + 32 * i, r = x / CH, c = x % CH;
-                        const bool ok = on && pos0 + r < t.nk;
+                        const bool ok = on && pos0 + r < most;
                         cp16(dk + (16 * u + r) * RB + swizzle_k<CH>(r, c) * 16, ok ? sk + r * (PAGED ? RB : a.k.st) + c * 16 : PAGED ? a.c.k : a.k.p, ok);
                         cp16(dv + (16 * u + r) * RB + swizzle_v<CH>(r, c) * 16, ok ? sv + r * (PAGED ? RB : a.v.st) + c * 16 : PAGED ? a.c.v : a.v.p, ok);
                     }
@@ -424,7 +424,7 @@ vdm_status launch(const AttnArgs& a, cudaStream_t s) {
     constexpr int M = ROWS8 ? 8 : RM;
     static std::atomic<uint64_t> ready{0};
     VDM_TRY(prepare_kernel(ready, reinterpret_cast<const void*>(kern), Cfg<D, SRC>::SMEM));
-    const int64_t tiles = (a.Tq * a.G + (a.B < a.Tq ? a.B : a.Tq) * (int64_t)(M - 1)) / M;
+    const int64_t tiles = row_tiles(a.Tq, a.G, a.B, M);
     VDM_TRY(launch_cluster(kern, dim3((unsigned)tiles, a.Hk, a.splits * a.cluster), RW * 32, Cfg<D, SRC>::SMEM, a.cluster, s, a, a.cluster));
     VDM_TRY(check_launch("attention_rows_kernel"));
     return a.splits > 1 ? launch_combine(a, VDM_BF16, s) : VDM_OK;

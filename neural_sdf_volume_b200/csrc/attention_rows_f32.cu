@@ -145,7 +145,7 @@ vdm_status launch(const AttnArgs& a, cudaStream_t s) {
     auto kern = attention_rows_f32_kernel<TC, D, PAGED, R>;
     static std::atomic<uint64_t> ready{0};
     VDM_TRY(prepare_kernel(ready, reinterpret_cast<const void*>(kern), 0));
-    const int64_t tiles = (a.Tq * a.G + (a.B < a.Tq ? a.B : a.Tq) * (int64_t)(R - 1)) / R;
+    const int64_t tiles = row_tiles(a.Tq, a.G, a.B, R);
     VDM_TRY(launch_cluster(kern, dim3((unsigned)tiles, a.Hk, a.splits * a.cluster), RW * 32, 0, a.cluster, s, a, a.cluster));
     VDM_TRY(check_launch("attention_rows_f32_kernel"));
     return a.splits > 1 ? launch_combine(a, VDM_F32, s) : VDM_OK;

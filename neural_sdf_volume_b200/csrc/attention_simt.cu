@@ -253,7 +253,7 @@ vdm_status launch(const AttnArgs& a, cudaStream_t s) {
     auto kern = attention_simt_kernel<T, TC, D, PAGED>;
     static std::atomic<uint64_t> ready{0};
     VDM_TRY(prepare_kernel(ready, reinterpret_cast<const void*>(kern), smem));
-    const int64_t tiles = (a.Tq * a.G + (a.B < a.Tq ? a.B : a.Tq) * (int64_t)(BR - 1)) / BR;
+    const int64_t tiles = row_tiles(a.Tq, a.G, a.B, BR);
     kern<<<dim3((unsigned)tiles, a.Hk, a.splits), ST, smem, s>>>(a);
     VDM_TRY(check_launch("attention_simt_kernel"));
     return a.splits > 1 ? launch_combine(a, sizeof(T) == 4 ? VDM_F32 : VDM_BF16, s) : VDM_OK;

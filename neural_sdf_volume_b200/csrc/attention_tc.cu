@@ -640,7 +640,7 @@ vdm_status launch(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& 
     auto kern = attention_tc_kernel<D, SRC>;
     static std::atomic<uint64_t> ready{0};
     VDM_TRY(prepare_kernel(ready, reinterpret_cast<const void*>(kern), smem_bytes<D>()));
-    const int64_t tiles = (a.Tq * a.G + (a.B < a.Tq ? a.B : a.Tq) * (int64_t)(tc_rows(D) - 1)) / tc_rows(D);
+    const int64_t tiles = row_tiles(a.Tq, a.G, a.B, tc_rows(D));
     kern<<<dim3((unsigned)tiles, a.Hk, a.splits), Cfg<D>::threads(SRC), smem_bytes<D>(), s>>>(mk, mv, a, tok_first);
     VDM_TRY(check_launch("attention_tc_kernel"));
     return a.splits > 1 ? launch_combine(a, VDM_BF16, s) : VDM_OK;

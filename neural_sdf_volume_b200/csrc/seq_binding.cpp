@@ -5,6 +5,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -50,6 +51,12 @@ const at::Tensor& tensor(const char* name, PyObject* o) {
     return t;
 }
 
+// nothing here has a backward pass: a call that would have to be differentiated is refused
+void no_grad(const char* name, const at::Tensor& t) {
+    if (t.requires_grad() && at::GradMode::is_enabled())
+        refuse("%s requires a gradient, which this call does not compute: detach it, or call under torch.no_grad()", name);
+}
+
 const at::Tensor& cuda_tensor(const char* name, PyObject* o) {
     const at::Tensor& t = tensor(name, o);
     if (!t.is_cuda()) refuse("%s must be a CUDA tensor (got one on %s)", name, t.device().str().c_str());
@@ -72,6 +79,7 @@ vdm_heads heads(const char* name, const at::Tensor& t, const at::Tensor& like, i
         refuse("%s must be %s (got %s)", name, c10::toString(like.scalar_type()), c10::toString(t.scalar_type()));
     if (t.device() != like.device())
         refuse("%s is on %s, the call's other tensors on %s", name, t.device().str().c_str(), like.device().str().c_str());
+    no_grad(name, t);
     if (t.size(1) > INT_MAX || t.size(2) > INT_MAX) refuse("%s: sizes %s do not fit", name, text(t.sizes()).c_str());
     if (t.numel() && t.size(2) > 1 && t.stride(2) != 1)
         refuse("%s: the elements of a head must be contiguous (stride %lld)", name, (long long)t.stride(2));
@@ -97,6 +105,7 @@ const float* gain(const char* name, PyObject* o, int64_t D, c10::Device dev) {
     const at::Tensor& g = tensor(name, o);
     if (g.scalar_type() != at::kFloat || g.dim() != 1 || g.size(0) != D || g.device() != dev || !g.is_contiguous())
         refuse("%s must be a contiguous float32 tensor of shape [%lld] on %s", name, (long long)D, dev.str().c_str());
+    no_grad(name, g);
     return static_cast<const float*>(g.data_ptr());
 }
 

@@ -64,8 +64,13 @@ __device__ __forceinline__ int cache_len(const CacheView& c, int32_t len) {
     return len < 0 ? 0 : len > cap ? (int)cap : len;
 }
 
+// Row tiles of M rows that a launch provides for: see find_tile.
+__host__ __device__ inline int64_t row_tiles(int64_t Tq, int G, int B, int M) { return Tq * G / M + B; }
+
 // Tile `idx` of the sequences' row tiles of M rows (whole warps, converged); false: no such tile.
 // With `last_first` a sequence's tiles come in descending order (causal: longest first).
+// Sequence b's tiles take the numbers from floor(cu[b] G / M) + b on - room for ceil(n G / M) of them
+// before the next sequence's - so that a tile's sequence is found by a search of the offsets.
 // Large tiles of up to 32 sequences come by the sequences' keys, longest first: a launch then ends
 // with its short blocks.
 __device__ __forceinline__ bool find_tile(const AttnArgs& a, int64_t idx, int M, bool last_first, RowTile& t) {
@@ -97,47 +102,28 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int64_t idx, int M,
         t.row0 = (int)((last_first ? cnt - 1 - local : local) * M);
         return true;
     }
-    int64_t done = 0;
-    int32_t lo[4], hi[4];   // offsets of the next 128 sequences, asked for together
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const int b = b0 + lane, part = (b0 >> 5) & 3;
-        if (part == 0) {
-#pragma unroll
-            for (int p = 0; p < 4; ++p)
-                if (b + 32 * p < a.B) lo[p] = a.cu_q[b + 32 * p], hi[p] = a.cu_q[b + 32 * p + 1];
-        }
-        int64_t start = 0;
-        int n = 0;
-        if (b < a.B) {
-            const int32_t l = part == 0 ? lo[0] : part == 1 ? lo[1] : part == 2 ? lo[2] : lo[3];
-            const int32_t h = part == 0 ? hi[0] : part == 1 ? hi[1] : part == 2 ? hi[2] : hi[3];
-            n = clamp_len(l, h, a.Tq, &start);
-        }
-        const int64_t tiles = ((int64_t)n * a.G + M - 1) / M;
-        int64_t incl = tiles;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += up;
-        }
-        const uint32_t m = __ballot_sync(0xffffffffu, done + incl > idx);
-        if (m) {
-            const int src = __ffs(m) - 1;
-            const int64_t before = done + __shfl_sync(0xffffffffu, incl - tiles, src);
-            const int64_t cnt = __shfl_sync(0xffffffffu, tiles, src);
-            t.b = b0 + src;
-            t.nq = __shfl_sync(0xffffffffu, n, src);
-            t.q0 = __shfl_sync(0xffffffffu, start, src);
-            const int64_t local = idx - before;
-            t.row0 = (int)((last_first ? cnt - 1 - local : local) * M);
-            t.k0 = 0;
-            if (a.paged) t.nk = cache_len(a.c, a.cu_k[t.b]);
-            else t.nk = clamp_len(a.cu_k[t.b], a.cu_k[t.b + 1], a.Tk, &t.k0);
-            return true;
-        }
-        done += __shfl_sync(0xffffffffu, incl, 31);
+    auto number = [&](int b) {
+        const int64_t c = a.cu_q[b];
+        return (c < 0 ? 0 : c > a.Tq ? a.Tq : c) * a.G / M + b;
+    };
+    int lo = 0, hi = a.B;   // in [lo, hi), 32 probes at a time
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, b = lo + lane * step;
+        const uint32_t m = __ballot_sync(0xffffffffu, b < hi && number(b) <= idx);
+        if (!m) return false;
+        lo += (31 - __clz(m)) * step;
+        hi = min(hi, lo + step);
     }
-    return false;
+    const int64_t local = idx - number(lo);
+    t.b = lo;
+    t.nq = clamp_len(a.cu_q[lo], a.cu_q[lo + 1], a.Tq, &t.q0);
+    const int64_t cnt = ((int64_t)t.nq * a.G + M - 1) / M;
+    if (local < 0 || local >= cnt) return false;
+    t.row0 = (int)((last_first ? cnt - 1 - local : local) * M);
+    t.k0 = 0;
+    if (a.paged) t.nk = cache_len(a.c, a.cu_k[lo]);
+    else t.nk = clamp_len(a.cu_k[lo], a.cu_k[lo + 1], a.Tk, &t.k0);
+    return true;
 }
 
 // keys that query token i of the tile's sequence sees: [0, result)

@@ -105,6 +105,7 @@ def cache(dt=2, pages=4, page=16, Hh=8, D=64, k=P, v=P, ks=P, vs=P):
 
 BAD_CACHES = [(1, dict(dt=3)), (2, dict(D=32)), (2, dict(page=8)), (2, dict(page=48)), (2, dict(page=512)), (1, dict(Hh=0)),
               (1, dict(pages=-1)), (1, dict(k=0)), (1, dict(v=P + 8)), (1, dict(ks=0)), (1, dict(vs=0))]
+BAD_CACHES += [(1, dict(ks=P + 8)), (1, dict(vs=P + 1))]             # scales are fetched 16 bytes at a time
 
 
 @pytest.mark.parametrize("status, kw", BAD_CACHES)
