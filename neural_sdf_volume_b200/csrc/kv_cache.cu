@@ -16,7 +16,7 @@
 namespace vdm {
 namespace {
 
-constexpr int CT = 128;
+constexpr int CT = 64;   // small blocks, twenty on an SM: 47 and 76 us for the prompts and contexts of 200 and 460 MB, 128 threads without a bound 50 and 85
 
 // Sequence that owns token t (offsets ascending), by a whole warp; -1: none.
 __device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int64_t t) {
@@ -28,6 +28,13 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int64_t t) 
         if (m != 0xffffffffu) break;
     }
     return b >= 0 && t < cu[b + 1] ? b : -1;
+}
+
+// bf16 pairs times a power of two
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
 
 // exponent of a row with largest finite magnitude m = f 2^E, f in [1/2, 1): 448 = 0.875 2^9, so that a
@@ -64,7 +71,7 @@ __device__ __forceinline__ uint32_t open8(const uint4 (&u)[2], float (&x)[8]) {
 }
 
 template <typename T, bool E4M3>
-__global__ void __launch_bounds__(CT) cache_write_kernel(const __grid_constant__ CacheIo a) {
+__global__ void __launch_bounds__(CT, 20) cache_write_kernel(const __grid_constant__ CacheIo a) {
     constexpr int W = (int)sizeof(T) / 2, U = 8 / W;   // 16-byte loads of 8 elements, pieces of 8 under way
     const int lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * (CT / 32) + (threadIdx.x >> 5);
@@ -111,24 +118,27 @@ __global__ void __launch_bounds__(CT) cache_write_kernel(const __grid_constant__
             }
             float x[8];
             uint32_t mb = open8(raw[u], x);
+            for (int o = 1; o < lph; o <<= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, o));
             if (__any_sync(0xffffffffu, mb >= 0x7f800000u)) {   // infinities become NaN, and neither counts
                 mb = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (!isfinite(x[i])) x[i] = __uint_as_float(0x7fc00000u);
-                    else mb = max(mb, __float_as_uint(fabsf(x[i])));
+                for (int e = 0; e < 8; ++e) {
+                    if (!isfinite(x[e])) x[e] = __uint_as_float(0x7fc00000u);
+                    else mb = max(mb, __float_as_uint(fabsf(x[e])));
                 }
+                for (int o = 1; o < lph; o <<= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, o));
             }
-            for (int o = 1; o < lph; o <<= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, o));
-            const float m = __uint_as_float(mb);
-            const int e = row_exponent(m);
-            const float inv = pow2i(-e);
+            const int e = row_exponent(__uint_as_float(mb));
+            const uint64_t inv = ptx::f32x2(pow2i(-e), pow2i(-e));
             uint32_t w[2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i] * inv, x[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-                const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2] * inv, x[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
-                w[i] = lo | (hi << 16);
+            for (int p = 0; p < 2; ++p) {
+                float y[4];
+                ptx::f32x2_split(ptx::mul_f32x2(ptx::f32x2(x[4 * p], x[4 * p + 1]), inv), y[0], y[1]);
+                ptx::f32x2_split(ptx::mul_f32x2(ptx::f32x2(x[4 * p + 2], x[4 * p + 3]), inv), y[2], y[3]);
+                const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
+                const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
+                w[p] = lo | (hi << 16);
             }
             if (on) {
                 *reinterpret_cast<uint2*>(dst + r * a.c.D + e0) = make_uint2(w[0], w[1]);
@@ -139,7 +149,7 @@ __global__ void __launch_bounds__(CT) cache_write_kernel(const __grid_constant__
 }
 
 template <typename TC, typename T>
-__global__ void __launch_bounds__(CT) cache_read_kernel(const __grid_constant__ CacheIo a) {
+__global__ void __launch_bounds__(CT, 20) cache_read_kernel(const __grid_constant__ CacheIo a) {
     constexpr bool E8 = sizeof(TC) == 1;
     constexpr int U = 8, N = 16 / (int)sizeof(T);   // pieces of 16 output bytes under way, elements of one
     const int lane = threadIdx.x & 31;
@@ -183,14 +193,21 @@ __global__ void __launch_bounds__(CT) cache_read_kernel(const __grid_constant__ 
             else {
                 const float s = scale_of(sc[u]);
                 const uint32_t w[2] = {raw[u].x, raw[u].y};
-                float x[N];
+                if constexpr (N == 8) {
+                    // a code has 4 significant bits: exact in bf16, and so is its product with a power of two
+                    const uint32_t ss = ptx::pack_bf16(s, s);
+                    uint32_t y[4];
 #pragma unroll
-                for (int i = 0; i < N; i += 4) {
-                    const float2 lo = e4m3x2_to_f((uint16_t)w[i / 4]), hi = e4m3x2_to_f((uint16_t)(w[i / 4] >> 16));
-                    x[i] = lo.x * s, x[i + 1] = lo.y * s, x[i + 2] = hi.x * s, x[i + 3] = hi.y * s;
+                    for (int p = 0; p < 2; ++p) {
+                        const float2 lo = e4m3x2_to_f((uint16_t)w[p]), hi = e4m3x2_to_f((uint16_t)(w[p] >> 16));
+                        y[2 * p] = mul_bf16x2(ptx::pack_bf16(lo.x, lo.y), ss);
+                        y[2 * p + 1] = mul_bf16x2(ptx::pack_bf16(hi.x, hi.y), ss);
+                    }
+                    *reinterpret_cast<uint4*>(d) = make_uint4(y[0], y[1], y[2], y[3]);
+                } else {
+                    const float2 lo = e4m3x2_to_f((uint16_t)w[0]), hi = e4m3x2_to_f((uint16_t)(w[0] >> 16));
+                    store4(reinterpret_cast<float*>(d), make_float4(lo.x * s, lo.y * s, hi.x * s, hi.y * s));
                 }
-                if constexpr (N == 8) *reinterpret_cast<uint4*>(d) = make_uint4(ptx::pack_bf16(x[0], x[1]), ptx::pack_bf16(x[2], x[3]), ptx::pack_bf16(x[4], x[5]), ptx::pack_bf16(x[6], x[7]));
-                else store4(reinterpret_cast<float*>(d), make_float4(x[0], x[1], x[2], x[3]));
             }
         }
     }

@@ -10,6 +10,7 @@
 // sincospif).  The norm is a shuffle sum inside the head's lanes.  Bound by memory: each element is
 // read once and written once.
 #include "seq_internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace vdm {
 namespace {
@@ -54,6 +55,7 @@ __global__ void __launch_bounds__(RT, 8) qk_norm_rope_kernel(const __grid_consta
     constexpr int N = Vec<T>::N, LPH = D / N, HPW = 32 / LPH;
     constexpr int NP = MODE >= 2 ? N : N / 2;   // angles of a lane: of each element, or of each pair
     __shared__ float s_cos[RT / 32][D / 2], s_sin[RT / 32][D / 2];
+    __shared__ __align__(16) float s_gain[2][D];
     __shared__ __align__(16) float s_row[RT / 32][HPW][MODE >= 2 ? D : 4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slot = warp / wpt, part = warp % wpt;
     const int64_t t = (int64_t)blockIdx.x * (RT / 32 / wpt) + slot;
@@ -74,8 +76,13 @@ __global__ void __launch_bounds__(RT, 8) qk_norm_rope_kernel(const __grid_consta
     };
     const int first = part * HPW + sub;
     load(first);
+    for (int i = threadIdx.x; i < D; i += RT) {
+        s_gain[0][i] = a.gq ? a.gq[i] : 1.0f;
+        s_gain[1][i] = a.gk ? a.gk[i] : 1.0f;
+    }
     float cs[NP], sn[NP];
-    if (MODE != 0) {
+    if (MODE == 0) __syncthreads();
+    else {
         if (live)
             for (int i = part * 32 + lane; i < half; i += 32 * wpt) {
                 double turns = (double)a.pos[t] * a.inv_freq[i] * 0.15915494309189533577;   // 1 / (2 pi)
@@ -105,16 +112,26 @@ __global__ void __launch_bounds__(RT, 8) qk_norm_rope_kernel(const __grid_consta
             float x[N];
             Vec<T>::open(raw[u], x);
             const bool isq = h < a.Hq;
-            const float* gain = isq ? a.gq : a.gk;
-            float ss = 0.f;
+            uint64_t sq = ptx::f32x2(0.f, 0.f);   // pairs of elements: half the instructions
 #pragma unroll
-            for (int i = 0; i < N; ++i) ss = fmaf(x[i], x[i], ss);
+            for (int i = 0; i < N; i += 2) {
+                const uint64_t p = ptx::f32x2(x[i], x[i + 1]);
+                sq = ptx::fma_f32x2(p, p, sq);
+            }
+            float ss, s1;
+            ptx::f32x2_split(sq, ss, s1);
+            ss += s1;
 #pragma unroll
             for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (gain) {
+            if (isq ? a.gq != nullptr : a.gk != nullptr) {
                 const float r = rsqrtf(ss * (1.0f / D) + a.eps);
+                const uint64_t rr = ptx::f32x2(r, r);
 #pragma unroll
-                for (int i = 0; i < N; ++i) x[i] = x[i] * r * __ldg(gain + e0 + i);
+                for (int i = 0; i < N; i += 4) {
+                    const float4 g = *reinterpret_cast<const float4*>(&s_gain[isq ? 0 : 1][e0 + i]);
+                    ptx::f32x2_split(ptx::mul_f32x2(ptx::mul_f32x2(ptx::f32x2(x[i], x[i + 1]), rr), ptx::f32x2(g.x, g.y)), x[i], x[i + 1]);
+                    ptx::f32x2_split(ptx::mul_f32x2(ptx::mul_f32x2(ptx::f32x2(x[i + 2], x[i + 3]), rr), ptx::f32x2(g.z, g.w)), x[i + 2], x[i + 3]);
+                }
             }
             if (MODE == 1) {
 #pragma unroll

@@ -114,15 +114,17 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int64_t idx, int M,
         lo += (31 - __clz(m)) * step;
         hi = min(hi, lo + step);
     }
-    const int64_t local = idx - number(lo);
+    // asked for together: these are a block's first loads, and everything waits for them
+    const int32_t q0 = a.cu_q[lo], q1 = a.cu_q[lo + 1], k0 = a.cu_k[lo], k1 = a.paged ? 0 : a.cu_k[lo + 1];
+    const int64_t local = idx - ((q0 < 0 ? 0 : q0 > a.Tq ? a.Tq : q0) * (int64_t)a.G / M + lo);
     t.b = lo;
-    t.nq = clamp_len(a.cu_q[lo], a.cu_q[lo + 1], a.Tq, &t.q0);
+    t.nq = clamp_len(q0, q1, a.Tq, &t.q0);
     const int64_t cnt = ((int64_t)t.nq * a.G + M - 1) / M;
     if (local < 0 || local >= cnt) return false;
     t.row0 = (int)((last_first ? cnt - 1 - local : local) * M);
     t.k0 = 0;
-    if (a.paged) t.nk = cache_len(a.c, a.cu_k[lo]);
-    else t.nk = clamp_len(a.cu_k[lo], a.cu_k[lo + 1], a.Tk, &t.k0);
+    if (a.paged) t.nk = cache_len(a.c, k0);
+    else t.nk = clamp_len(k0, k1, a.Tk, &t.k0);
     return true;
 }
 
