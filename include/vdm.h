@@ -571,11 +571,12 @@ VDM_API vdm_status vdm_attention_paged(const vdm_attention* a, const vdm_heads* 
 VDM_API vdm_status vdm_attention_status(vdm_stream stream);
 
 /* Test hook for failure detection (not needed for decoding).  mode n >= 1
- * makes the n-th tensor-core decode launch from now on (1 = the next one)
- * withhold one completion signal, so its warps run into their bounded waits;
+ * makes the n-th tensor-core decode or attention launch from now on (1 = the
+ * next one) withhold completion signals, so its warps run into their bounded waits;
  * `timeout_cycles` (> 0) shortens those waits.  The call that made that
  * launch returns VDM_ERR_TIMEOUT (a hierarchical call checks after each
- * level's marking and at its end) and the CUDA context stays usable.  mode 0
+ * level's marking and at its end; an attention call does not wait, its timeout
+ * is vdm_attention_status's) and the CUDA context stays usable.  mode 0
  * restores normal operation.                                                */
 VDM_API vdm_status vdm_debug_inject(int32_t mode, int64_t timeout_cycles);
 

@@ -705,7 +705,7 @@ def vdm_surface_case_table():
 
 def vdm_debug_inject(mode: int, timeout_cycles: int = 0):
     """Test hook: mode 1 withholds one completion signal in the next
-    tensor-core decode launch (its bounded waits then report a timeout)."""
+    tensor-core decode or attention launch (its bounded waits then report a timeout)."""
     _check(_lib.vdm_debug_inject(mode, timeout_cycles))
 
 

@@ -436,7 +436,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 const uint64_t off = (uint64_t)((kk >> 2) * (BN * 128 / 16) + (kk & 3) * 2);
                 mma_ss_w(tmem + 128 * w, dq + off, dk + off, id_s, kk > 0);
             }
-            mma_commit_w(smem_u32(&sh.s_full[w]));
+            if (!a.withhold) mma_commit_w(smem_u32(&sh.s_full[w]));
         };
         auto issue_pv = [&](int w, int i, uint32_t slot) {
             if (!wait(C::EARLY ? &sh.p_half[w] : &sh.p_full[w], i & 1, 6)) return false;

@@ -194,7 +194,11 @@ vdm_status run_attention(const vdm_attention* at, AttnArgs& a, int64_t max_kv, c
     a.part_o = static_cast<float*>(ws);
     a.part_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + up256((size_t)a.splits * a.Tq * at->Hq * at->D * 4));
     VDM_TRY(attention_error_word(&a.err));
-    a.timeout = 4000000000ll;   // cycles of one bounded wait, about two seconds
+    a.timeout = g_debug.timeout > 0 ? g_debug.timeout : 4000000000ll;   // cycles of one bounded wait, about two seconds
+    if (plan.kernel == kTc) {   // test hook: the g_debug.inject-th launch from the hook's call withholds one signal
+        a.withhold = g_debug.inject == 1;
+        if (g_debug.inject > 0) --g_debug.inject;
+    }
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (plan.kernel == kRows) return launch_attention_rows(a, st);
     if (plan.kernel == kRowsF32) return launch_attention_rows_f32(a, st);

@@ -41,6 +41,7 @@ struct AttnArgs {
     int cluster;             // few rows: blocks that share a tile's keys and join in shared memory
     int* err;                // error word of bounded waits
     long long timeout;
+    int withhold;            // test hook: one completion signal of the tensor-core kernel is not given
 };
 
 // One block of query rows of one sequence and key head.  Rows are (token, query head of the

@@ -253,7 +253,34 @@ def test_cache_beyond_32_bit_offsets(kind):
     close(one, np64(near)[-1:], 2 * tol[-1:])
 
 
-# ----------------------------------------------------------------- graphs, gradients
+# ----------------------------------------------------------------- failure detection, graphs, gradients
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kind", ["packed", "bf16", "e4m3"])
+def test_withheld_signal_times_out_and_later_calls_run(D, kind):
+    """A tensor-core attention whose scores are never announced gives up its waits; the status says so once."""
+    n = 2000                                       # enough for the tensor-core kernel
+    q = randn(1, n, 8, D)
+    if kind == "packed":
+        k, v = randn(2, n, 2, D), randn(3, n, 2, D)
+        call = lambda: vdm.vdm_attention_packed(q, k, v, offsets([n]))
+    else:
+        c = S.Cached(kind, 2, D, 32, [n], seed=1)
+        call = lambda: vdm.vdm_attention_paged(q, c.cache, offsets([n]), c.kv_len, c.table)
+    want = call()
+    vdm.vdm_attention_status()
+    vdm.vdm_debug_inject(1, 20_000_000)            # cycles of a wait, about 10 ms
+    try:
+        call()
+        with pytest.raises(vdm.VdmError) as e:
+            vdm.vdm_attention_status()
+        assert e.value.status == 5 and "bounded wait" in str(e.value)
+    finally:
+        vdm.vdm_debug_inject(0, 0)
+    vdm.vdm_attention_status()
+    assert torch.equal(call(), want)
+    vdm.vdm_attention_status()
+
 
 def test_two_graphs_and_an_eager_call_at_once():
     """Captured calls keep workspaces of their own: two graphs replayed on two streams beside an eager call."""
