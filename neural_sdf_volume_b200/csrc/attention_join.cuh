@@ -19,108 +19,140 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
     return v;
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t a) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a));
-    return v;
+__device__ __forceinline__ void st_cluster_f32(uint32_t a, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t a) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
-    return v;
+__device__ __forceinline__ void st_cluster_f4(uint32_t a, float4 v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+// "this block runs", told to the cluster early and asked for before the first write into another block
+__device__ __forceinline__ void cluster_started() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// repair_row out of line: the few-row kernels run their code once, and what they do not run is better elsewhere
+template <typename TC, int D, bool PAGED>
+__device__ __noinline__ float repair_row_apart(const AttnArgs& a, const RowTile& t, int hk, int row, int j0, int j1, float4& o) {
+    return repair_row<TC, D, PAGED>(a, t, hk, row, j0, j1, o);
 }
 
-// A row's parts of the block's warps as one: maximum (result), sum and elements.
-template <int WARP>
-__device__ __forceinline__ float join_warps(const float (&sm)[RW][RM], const float (&sl)[RW][RM], uint32_t at, int row, bool on, float& L, float4& x) {
-    float M = -INFINITY;
+// Parts of a lane's row (row = lane % 16) as factors of one sum: maxima pm, sums pl -> factors f, sum L; returns the
+// maximum, 0 for -inf.
+template <int P>
+__device__ __forceinline__ float join_factors(const float (&pm)[P], const float (&pl)[P], float (&f)[P], float& L) {
+    float M = pm[0];
 #pragma unroll
-    for (int w = 0; w < RW; ++w) M = fmaxf(M, sm[w][row]);
+    for (int p = 1; p < P; ++p) M = fmaxf(M, pm[p]);
     const float ref = M == -INFINITY ? 0.f : M;
     L = 0.f;
-    x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < RW; ++w) {
-        const float pm = sm[w][row], pl = sl[w][row];
-        const float f = pm == -INFINITY && pl == 0.f ? 0.f : exp2f(pm - ref);
-        L = fmaf(f, pl, L);
-        if (on) {
-            const uint4 y = lds128(at + w * WARP);
-            x.x = fmaf(f, __uint_as_float(y.x), x.x), x.y = fmaf(f, __uint_as_float(y.y), x.y);
-            x.z = fmaf(f, __uint_as_float(y.z), x.z), x.w = fmaf(f, __uint_as_float(y.w), x.w);
-        }
+    for (int p = 0; p < P; ++p) {
+        f[p] = pm[p] == -INFINITY && pl[p] == 0.f ? 0.f : exp2f(pm[p] - ref);   // no key: nothing
+        L = fmaf(f[p], pl[p], L);
     }
-    return M;
+    return ref;
 }
 
-// Rows row * D floats at part + w WARP of warp w.  Keys [j0, j1) are the ones of this split; a row that sees
-// fewer of them and ends up not finite is computed again (REPAIR).
-template <typename T, typename TC, int D, bool PAGED, int WARP, bool REPAIR>
+__device__ __forceinline__ void add_part(float4& x, float f, const float4& y) {
+    x.x = fmaf(f, y.x, x.x), x.y = fmaf(f, y.y, x.y), x.z = fmaf(f, y.z, x.z), x.w = fmaf(f, y.w, x.w);
+}
+
+// Rows row * D floats at part + w WARP of warp w.  What is one number a row (maxima, factors, addresses) is
+// computed for all rows at once, a lane each; then a warp adds up its rows' elements.  In a cluster block b
+// finishes the rows b, b + n, ...: the others write their parts of them into its shared memory, so that one
+// barrier is enough (reading them there took a second one, before a block may leave, and 2 us in all).
+// Keys [j0, j1) are the ones of this split; a row that sees fewer of them and ends up not finite is computed
+// again (REPAIR).  ROWS: rows of a tile, at most.
+template <typename T, typename TC, int D, bool PAGED, int WARP, int ROWS, bool REPAIR>
 __device__ __forceinline__ void join_rows(const AttnArgs& a, const RowTile& t, int hk, int split, int rank, int cluster, int n_rows, int j0,
                                           int j1, float (&s_m)[RW][RM], float (&s_l)[RW][RM], uint32_t part) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int MAXC = 8;                          // blocks of a cluster, at most
+    constexpr int TAKE = ROWS > MAXC ? ROWS : MAXC;  // rows that come in: a row of every block for each of its own
+    __shared__ __align__(16) float s_in[TAKE][D];
+    __shared__ float s_mi[TAKE], s_li[TAKE];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mine = lane & (RM - 1);
     const bool on = 4 * lane < D;
+    const uint32_t at = part + 16 * lane;
     __syncthreads();
+    float fw[RW], L, ref;
+    {
+        float pm[RW], pl[RW];
+#pragma unroll
+        for (int w = 0; w < RW; ++w) pm[w] = s_m[w][mine], pl[w] = s_l[w][mine];
+        ref = join_factors(pm, pl, fw, L);
+    }
+    auto warps_sum = [&](int row) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < RW; ++w) {
+            const float f = __shfl_sync(0xffffffffu, fw[w], row);
+            if (on) {
+                const uint4 y = lds128(at + w * WARP + row * D * 4);
+                add_part(x, f, make_float4(__uint_as_float(y.x), __uint_as_float(y.y), __uint_as_float(y.z), __uint_as_float(y.w)));
+            }
+        }
+        return x;
+    };
+    // row -> block row % cluster, its row / cluster -th; that block's place for part k: k own + row / cluster
+    const int own = (ROWS + cluster - 1) / cluster;
     if (cluster > 1) {
+        cluster_wait();
         for (int row = warp; row < n_rows; row += RW) {
-            float L;
-            float4 x;
-            const float M = join_warps<WARP>(s_m, s_l, part + (row * D + 4 * lane) * 4, row, on, L, x);
-            __syncwarp();
-            if (on)
-                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(part + (row * D + 4 * lane) * 4), "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w) : "memory");
-            if (lane == 0) s_m[0][row] = M, s_l[0][row] = L;
+            const float4 x = warps_sum(row);
+            if (on) st_cluster_f4(ptx::mapa(ptx::smem_u32(&s_in[rank * own + row / cluster][4 * lane]), row % cluster), x);
+        }
+        if (warp == 0 && lane < n_rows) {   // no key: -inf and 0
+            const int place = rank * own + mine / cluster;
+            st_cluster_f32(ptx::mapa(ptx::smem_u32(&s_mi[place]), mine % cluster), L == 0.f ? -INFINITY : ref);
+            st_cluster_f32(ptx::mapa(ptx::smem_u32(&s_li[place]), mine % cluster), L);
         }
         ptx::cluster_sync();
     }
-    for (int row = rank * RW + warp; row < n_rows; row += cluster * RW) {
-        float L = 0.f, ref;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (cluster == 1) {
-            const float M = join_warps<WARP>(s_m, s_l, part + (row * D + 4 * lane) * 4, row, on, L, x);
-            ref = M == -INFINITY ? 0.f : M;
-        } else {
-            // lane k: block k's maximum and sum
-            float pm = -INFINITY, pl = 0.f;
-            if (lane < cluster) {
-                pm = ld_cluster_f32(ptx::mapa(ptx::smem_u32(&s_m[0][row]), lane));
-                pl = ld_cluster_f32(ptx::mapa(ptx::smem_u32(&s_l[0][row]), lane));
-            }
-            float M = pm;
+    // from here a lane's row is the mine-th of the block's own (all rows without a cluster)
+    const int n_own = cluster == 1 ? n_rows : (n_rows - rank + cluster - 1) / cluster;
+    float fc[MAXC];
+    if (cluster > 1) {
+        float pm[MAXC], pl[MAXC];
 #pragma unroll
-            for (int w = 16; w; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
-            ref = M == -INFINITY ? 0.f : M;
-            const float pf = pm == -INFINITY && pl == 0.f ? 0.f : exp2f(pm - ref);   // no key: nothing
-#pragma unroll 4
-            for (int k = 0; k < cluster; ++k) {
-                const float f = __shfl_sync(0xffffffffu, pf, k);
-                L = fmaf(f, __shfl_sync(0xffffffffu, pl, k), L);
-                if (on) {
-                    const float4 y = ld_cluster_f4(ptx::mapa(part + (row * D + 4 * lane) * 4, k));
-                    x.x = fmaf(f, y.x, x.x), x.y = fmaf(f, y.y, x.y), x.z = fmaf(f, y.z, x.z), x.w = fmaf(f, y.w, x.w);
-                }
+        for (int k = 0; k < MAXC; ++k) {
+            const bool there = k < cluster && mine < n_own;
+            pm[k] = there ? s_mi[k * own + mine] : -INFINITY;
+            pl[k] = there ? s_li[k * own + mine] : 0.f;
+        }
+        ref = join_factors(pm, pl, fc, L);
+    }
+    const float inv = L == 0.f ? 0.f : 1.0f / L, lse2 = L == 0.f ? -INFINITY : ref + log2f(L);
+    const int rr = t.row0 + min(mine * cluster + rank, n_rows - 1), see = keys_seen(a, t, rr / a.G), h = hk * a.G + rr % a.G;
+    const int64_t tok = t.q0 + rr / a.G, prow = ((int64_t)split * a.Tq + tok) * a.Hq + h;
+    const bool parts = a.splits > 1;
+    char* const dst = parts ? reinterpret_cast<char*>(a.part_o + prow * D) : a.out.p + tok * a.out.st + h * a.out.sh;
+    if (warp == 0 && lane < n_own) {
+        if (parts) a.part_lse[prow] = lse2;
+        else if (a.lse) a.lse[tok * a.Hq + h] = lse2 * kLn2;
+    }
+    for (int row = warp; row < n_own; row += RW) {
+        float4 x;
+        if (cluster == 1) x = warps_sum(row);
+        else {
+            x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < MAXC; ++k) {
+                const float f = __shfl_sync(0xffffffffu, fc[k], row);
+                if (k < cluster && on) add_part(x, f, *reinterpret_cast<const float4*>(&s_in[k * own + row][4 * lane]));
             }
         }
-        const float inv = L == 0.f ? 0.f : 1.0f / L;
-        x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
-        float lse2 = L == 0.f ? -INFINITY : ref + log2f(L);
-        const int rr = t.row0 + row, see = keys_seen(a, t, rr / a.G);
+        const float i = __shfl_sync(0xffffffffu, inv, row);
+        x.x *= i, x.y *= i, x.z *= i, x.w *= i;
+        char* const p = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), row));
         if (REPAIR) {
+            const int end = min(__shfl_sync(0xffffffffu, see, row), j1);
             const bool bad = !(fabsf(x.x) < INFINITY && fabsf(x.y) < INFINITY && fabsf(x.z) < INFINITY && fabsf(x.w) < INFINITY);
-            if (see < j1 && __any_sync(0xffffffffu, bad)) lse2 = repair_row<TC, D, PAGED>(a, t, hk, rr, j0, min(see, j1), x);
+            if (end < j1 && __any_sync(0xffffffffu, bad)) repair_row_apart<TC, D, PAGED>(a, t, hk, t.row0 + row * cluster + rank, j0, end, x);
         }
-        const int64_t tok = t.q0 + rr / a.G;
-        const int h = hk * a.G + rr % a.G;
-        if (a.splits > 1) {
-            const int64_t prow = ((int64_t)split * a.Tq + tok) * a.Hq + h;
-            if (on) store4(a.part_o + prow * D + 4 * lane, x);
-            if (lane == 0) a.part_lse[prow] = lse2;
-        } else {
-            if (on) store4(reinterpret_cast<T*>(a.out.p + tok * a.out.st + h * a.out.sh) + 4 * lane, x);
-            if (lane == 0 && a.lse) a.lse[tok * a.Hq + h] = lse2 * kLn2;
+        if (on) {
+            if (parts) store4(reinterpret_cast<float*>(p) + 4 * lane, x);
+            else store4(reinterpret_cast<T*>(p) + 4 * lane, x);
         }
     }
-    if (cluster > 1) ptx::cluster_sync();   // no block leaves while another reads its shared memory
 }
 
 // a launch whose blocks along z form clusters

@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(RW * 32, 3) attention_rows_kernel(const __grid
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     RowTile t;
     if (!find_tile(a, blockIdx.x, ROWS8 ? 8 : RM, a.causal, t)) return;   // the whole cluster alike
+    if (cluster > 1) cluster_started();
     const int hk = blockIdx.y, rank = blockIdx.z % cluster, split = blockIdx.z / cluster;
     const int n_rows = min(ROWS8 ? 8 : RM, t.nq * a.G - t.row0);
 
@@ -126,6 +127,21 @@ __global__ void __launch_bounds__(RW * 32, 3) attention_rows_kernel(const __grid
     const int n_steps = (most + KS - 1) / KS, per = (n_steps + a.splits - 1) / a.splits;
     const int s0 = min(n_steps, split * per), s1 = min(n_steps, s0 + per);
     const int first = s0 + rank * RW + warp, stride = cluster * RW;
+
+    // Queries, asked for first: row 8 r + g; the pairs of k-step kk of lane t4 are elements 4 i + {0, 1} and
+    // {2, 3} of the row's 16-byte (in the keys' type) chunk t4 + 4 h.
+    uint2 raw[KK][NQ];
+#pragma unroll
+    for (int r = 0; r < NQ; ++r) {
+        const bool on = g + 8 * r < n_rows;
+        const int rr = t.row0 + (on ? g + 8 * r : 0);
+        const char* q = a.q.p + (t.q0 + rr / a.G) * a.q.st + (int64_t)(hk * a.G + rr % a.G) * a.q.sh;
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) {
+            const int h = kk / (EC / 4), i = kk % (EC / 4);
+            raw[kk][r] = on ? *reinterpret_cast<const uint2*>(q + ((t4 + 4 * h) * EC + 4 * i) * 2) : make_uint2(0u, 0u);
+        }
+    }
 
     const uint32_t ring = smem_u32(dyn) + warp * C::WARP;
     constexpr int U = KS / 16;   // a page holds whole blocks of 16 keys
@@ -184,40 +200,30 @@ __global__ void __launch_bounds__(RW * 32, 3) attention_rows_kernel(const __grid
     }
     pages_of(first + (NS - 1) * stride, pg);
 
-    // queries as fragments, row 8 r + g: the pairs of k-step kk of lane t4 are elements
-    // 4 i + {0, 1} and {2, 3} of the row's 16-byte (in the keys' type) chunk t4 + 4 h
+    // queries as fragments
     uint32_t qb[KK][NQ][2];
     float rs[NQ][2];     // rows 8 r + 2 t4 + j: factor of the scores (softmax scale, log2 e, Q's exponent)
     int seen[NQ][2];     // and the keys that the row sees
 #pragma unroll
     for (int r = 0; r < NQ; ++r) {
-        const int row = g + 8 * r;
-        const bool on = row < n_rows;
-        const int rr = t.row0 + (on ? row : 0);
-        const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q.p + (t.q0 + rr / a.G) * a.q.st +
-                                                                        (int64_t)(hk * a.G + rr % a.G) * a.q.sh);
         float mul = 1.0f, back = a.scale_log2;
         if (E8) {
-            float mx = 0.f;
-            if (on)
-                for (int i = t4 * (D / 4); i < (t4 + 1) * (D / 4); i += 4) {
-                    const float4 x = load4f(q + i);
-                    mx = fmax3(fmax3(mx, fabsf(x.x), fabsf(x.y)), fabsf(x.z), fabsf(x.w));
-                }
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            // exponent e of the maximum (2^e <= mx < 2^(e+1)); Q' = Q 2^(14 - e)
-            const int e = mx > 0.f ? (int)(__float_as_uint(mx) >> 23) - 127 : 14, up = min(14 - e, 120);
+            uint32_t mx = 0;   // largest magnitude, bits of a bf16 in either half
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) mx = __vmaxu2(mx, __vmaxu2(raw[kk][r].x & 0x7fff7fffu, raw[kk][r].y & 0x7fff7fffu));
+            mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            // exponent e of the maximum (2^e <= it < 2^(e+1); infinities and NaN: 128); Q' = Q 2^(14 - e)
+            const uint32_t top = max(mx << 16, mx & 0xffff0000u);
+            const int e = top ? (int)(top >> 23) - 127 : 14, up = min(14 - e, 120);
             mul = pow2i(up);
             back *= pow2i(-up);
         }
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
-            const int h = kk / (EC / 4), i = kk % (EC / 4), d = (t4 + 4 * h) * EC + 4 * i;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (on) x = load4f(q + d);
-            qb[kk][r][0] = E8 ? pack_f16(x.x * mul, x.y * mul) : pack_bf16(x.x, x.y);
-            qb[kk][r][1] = E8 ? pack_f16(x.z * mul, x.w * mul) : pack_bf16(x.z, x.w);
+            const uint2 x = raw[kk][r];
+            qb[kk][r][0] = E8 ? pack_f16(__uint_as_float(x.x << 16) * mul, __uint_as_float(x.x & 0xffff0000u) * mul) : x.x;
+            qb[kk][r][1] = E8 ? pack_f16(__uint_as_float(x.y << 16) * mul, __uint_as_float(x.y & 0xffff0000u) * mul) : x.y;
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -414,7 +420,7 @@ __global__ void __launch_bounds__(RW * 32, 3) attention_rows_kernel(const __grid
                 asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(ring + (row * D + d) * 4), "f"(o[i][r][j] * w0), "f"(o[i][r][2 + j] * w0) : "memory");
             }
         }
-    join_rows<__nv_bfloat16, typename std::conditional<E8, uint8_t, __nv_bfloat16>::type, D, PAGED, C::WARP, true>(
+    join_rows<__nv_bfloat16, typename std::conditional<E8, uint8_t, __nv_bfloat16>::type, D, PAGED, C::WARP, ROWS8 ? 8 : 16, true>(
         a, t, hk, split, rank, cluster, n_rows, s0 * KS, min(s1 * KS, most), s_m, s_l, smem_u32(dyn));
 }
 

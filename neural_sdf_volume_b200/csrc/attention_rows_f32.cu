@@ -23,6 +23,7 @@ __global__ void __launch_bounds__(RW * 32) attention_rows_f32_kernel(const __gri
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane >> 3, c = lane & 7;
     RowTile t;
     if (!find_tile(a, blockIdx.x, R, a.causal, t)) return;   // the whole cluster alike
+    if (cluster > 1) cluster_started();
     const int hk = blockIdx.y, rank = blockIdx.z % cluster, split = blockIdx.z / cluster;
     const int n_rows = min(R, t.nq * a.G - t.row0);
     const int most = keys_seen(a, t, (t.row0 + n_rows - 1) / a.G);
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(RW * 32) attention_rows_f32_kernel(const __gri
 #pragma unroll
             for (int i = 0; i < NI; ++i) *reinterpret_cast<float4*>(&s_part[warp][r][dim(i)]) = o[r][i];
     }
-    join_rows<float, TC, D, PAGED, WARP, false>(a, t, hk, split, rank, cluster, n_rows, 0, 0, s_m, s_l, ptx::smem_u32(&s_part[0][0][0]));
+    join_rows<float, TC, D, PAGED, WARP, R, false>(a, t, hk, split, rank, cluster, n_rows, 0, 0, s_m, s_l, ptx::smem_u32(&s_part[0][0][0]));
 }
 
 template <typename TC, int D, bool PAGED, int R>
