@@ -48,47 +48,62 @@ __global__ void __launch_bounds__(RW * 32) attention_rows_f32_kernel(const __gri
         m[r] = -INFINITY;
         l[r] = 0.f;
     }
-    const KvRows<TC, PAGED> kv{a, t, hk};
-    for (int step = s0 + rank * RW + warp; step < s1; step += cluster * RW) {
+    // a lane's share of a key and its value, as stored; zeros where there is no key or no page
+    struct Step {
+        float4 k[E8 ? 1 : NI], v[E8 ? 1 : NI];
+        uint32_t kc[E8 ? NI : 1], vc[E8 ? NI : 1];   // codes
+        uint8_t ks, vs;
+    };
+    auto fetch = [&](Step& x, int step) {
         const int key = 4 * step + j;
-        float4 k[NI], v[NI];
-        bool there = key < most;
-        if constexpr (PAGED) {
-            const int64_t row = there ? cache_row(a.c, t.b, hk, key) : -1;
+        int64_t row = -1;
+        if (step < s1 && key < most) row = PAGED ? cache_row(a.c, t.b, hk, key) : t.k0 + key;
+        if constexpr (E8) {
+            x.ks = x.vs = 127;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) x.kc[i] = x.vc[i] = 0u;
             if (row >= 0) {
-                const TC *pk = reinterpret_cast<const TC*>(a.c.k) + row * D, *pv = reinterpret_cast<const TC*>(a.c.v) + row * D;
-                float fk = 1.f, fv = 1.f;
-                if (E8) fk = scale_of(a.c.ks[row]), fv = scale_of(a.c.vs[row]);
+                const char *pk = a.c.k + row * D + dim(0), *pv = a.c.v + row * D + dim(0);
 #pragma unroll
-                for (int i = 0; i < NI; ++i) k[i] = load4f(pk + dim(i)), v[i] = load4f(pv + dim(i));
-                if (E8)
-#pragma unroll
-                    for (int i = 0; i < NI; ++i) {
-                        k[i].x *= fk, k[i].y *= fk, k[i].z *= fk, k[i].w *= fk;
-                        v[i].x *= fv, v[i].y *= fv, v[i].z *= fv, v[i].w *= fv;
-                    }
-            } else {
-#pragma unroll
-                for (int i = 0; i < NI; ++i) k[i] = v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int i = 0; i < NI; i += 2) {
+                    const uint2 ck = *reinterpret_cast<const uint2*>(pk + 4 * i), cv = *reinterpret_cast<const uint2*>(pv + 4 * i);
+                    x.kc[i] = ck.x, x.kc[i + 1] = ck.y, x.vc[i] = cv.x, x.vc[i + 1] = cv.y;
+                }
+                x.ks = a.c.ks[row], x.vs = a.c.vs[row];
             }
         } else {
+            const char *pk = PAGED ? a.c.k + row * (D * 4) : a.k.p + row * a.k.st + hk * a.k.sh;
+            const char *pv = PAGED ? a.c.v + row * (D * 4) : a.v.p + row * a.v.st + hk * a.v.sh;
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                k[i] = v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (there) k[i] = kv.get(false, key, dim(i)), v[i] = kv.get(true, key, dim(i));
+                x.k[i] = x.v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (row >= 0) x.k[i] = load4f(reinterpret_cast<const float*>(pk) + dim(i)), x.v[i] = load4f(reinterpret_cast<const float*>(pv) + dim(i));
             }
         }
+    };
+    auto use = [&](const Step& x, int step) {
+        const int key = 4 * step + j;
+        const float fk = E8 ? scale_of(x.ks) : 1.f, fv = E8 ? scale_of(x.vs) : 1.f;
         float s[R];
         bool raise = false;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            float x = 0.f;
+        for (int r = 0; r < R; ++r) s[r] = 0.f;
 #pragma unroll
-            for (int i = 0; i < NI; ++i) x = fmaf(q[r][i].x, k[i].x, fmaf(q[r][i].y, k[i].y, fmaf(q[r][i].z, k[i].z, fmaf(q[r][i].w, k[i].w, x))));
-            x += __shfl_xor_sync(0xffffffffu, x, 1);
-            x += __shfl_xor_sync(0xffffffffu, x, 2);
-            x += __shfl_xor_sync(0xffffffffu, x, 4);
-            s[r] = key < seen[r] ? x * a.scale_log2 : -INFINITY;
+        for (int i = 0; i < NI; ++i) {
+            float4 k;
+            if constexpr (E8) {
+                const float2 lo = e4m3x2_to_f((uint16_t)x.kc[i]), hi = e4m3x2_to_f((uint16_t)(x.kc[i] >> 16));
+                k = make_float4(lo.x * fk, lo.y * fk, hi.x * fk, hi.y * fk);
+            } else k = x.k[i];
+#pragma unroll
+            for (int r = 0; r < R; ++r) s[r] = fmaf(q[r][i].x, k.x, fmaf(q[r][i].y, k.y, fmaf(q[r][i].z, k.z, fmaf(q[r][i].w, k.w, s[r]))));
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            s[r] += __shfl_xor_sync(0xffffffffu, s[r], 1);
+            s[r] += __shfl_xor_sync(0xffffffffu, s[r], 2);
+            s[r] += __shfl_xor_sync(0xffffffffu, s[r], 4);
+            s[r] = key < seen[r] ? s[r] * a.scale_log2 : -INFINITY;
             raise = raise || s[r] > m[r];
         }
         if (__any_sync(0xffffffffu, raise)) {
@@ -101,18 +116,39 @@ __global__ void __launch_bounds__(RW * 32) attention_rows_f32_kernel(const __gri
                 for (int i = 0; i < NI; ++i) o[r][i].x *= f, o[r][i].y *= f, o[r][i].z *= f, o[r][i].w *= f;
             }
         }
+        float p[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            if (key >= seen[r]) continue;
-            const float p = exp2f(s[r] - (m[r] == -INFINITY ? 0.f : m[r]));
-            l[r] += p;
+            p[r] = 0.f;
+            if (key < seen[r]) p[r] = exp2f(s[r] - (m[r] == -INFINITY ? 0.f : m[r])), l[r] += p[r];
+        }
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                o[r][i].x = fmaf(p, v[i].x, o[r][i].x), o[r][i].y = fmaf(p, v[i].y, o[r][i].y);
-                o[r][i].z = fmaf(p, v[i].z, o[r][i].z), o[r][i].w = fmaf(p, v[i].w, o[r][i].w);
+        for (int i = 0; i < NI; ++i) {
+            float4 v;
+            if constexpr (E8) {
+                const float2 lo = e4m3x2_to_f((uint16_t)x.vc[i]), hi = e4m3x2_to_f((uint16_t)(x.vc[i] >> 16));
+                v = make_float4(lo.x * fv, lo.y * fv, hi.x * fv, hi.y * fv);
+            } else v = x.v[i];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (key >= seen[r]) continue;
+                o[r][i].x = fmaf(p[r], v.x, o[r][i].x), o[r][i].y = fmaf(p[r], v.y, o[r][i].y);
+                o[r][i].z = fmaf(p[r], v.z, o[r][i].z), o[r][i].w = fmaf(p[r], v.w, o[r][i].w);
             }
         }
-        __syncwarp();
+    };
+    // two steps under way
+    const int stride = cluster * RW;
+    Step x0, x1;
+    int step = s0 + rank * RW + warp;
+    fetch(x0, step);
+    while (step < s1) {
+        fetch(x1, step + stride);
+        use(x0, step);
+        if (step + stride >= s1) break;
+        fetch(x0, step + 2 * stride);
+        use(x1, step + stride);
+        step += 2 * stride;
     }
     // the four groups as one, in a fixed order
 #pragma unroll

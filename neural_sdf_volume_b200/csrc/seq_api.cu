@@ -158,11 +158,12 @@ Plan plan_attention(const vdm_attention* at, int B, int64_t Tq, int64_t max_kv) 
     if (4.0 + (double)few * steps * share * few_step / (148 * 12) < best) {
         p.kernel = bf16 ? kRows : kRowsF32;
         p.splits = 1;
-        // Blocks of a tile: one where its warps have three steps or fewer (a cluster's joining takes 2 us); else until
+        // Blocks of a tile: one where its warps have three steps (float32: half a step) or fewer, for a cluster's
+        // joining takes 2 us; else until
         // the SMs are full and a warp has half a step, or, for the sake of ragged lengths, until there are some
         // 1500 with at least 16 steps a warp.
         const int64_t full = bf16 || at->D == 64 ? 512 : 296;
-        while (steps > 12 && p.cluster < 8 && ((few * p.cluster * 2 <= full && p.cluster * 4 <= steps) || (few * p.cluster < 1500 && p.cluster * 128 <= steps)))
+        while (steps > (bf16 ? 12 : 2) && p.cluster < 8 && ((few * p.cluster * 2 <= full && p.cluster * 4 <= steps) || (few * p.cluster < 1500 && p.cluster * 128 <= steps)))
             p.cluster *= 2;
         if (p.cluster == 8)
             while (p.splits < 16 && few * 8 * p.splits < 296 && p.splits * 192 <= steps) p.splits *= 2;
