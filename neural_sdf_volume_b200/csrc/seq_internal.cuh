@@ -129,6 +129,16 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int64_t idx, int M,
     return true;
 }
 
+// Key head and tile number of a block of grid x = tiles x heads.  Packed: the heads of a tile beside one
+// another, so that blocks start in the order of their lengths, whatever their head (packed_vecsets 111 us,
+// head after head 120; packed_prompts 356 and 368).  Paged: a head's tiles beside one another, since contexts
+// are long and a head's tiles then meet its keys in the cache (paged_chunk 218 us, the other way 228).
+__device__ __forceinline__ int64_t head_of(const AttnArgs& a, int& hk) {
+    const unsigned n = a.paged ? gridDim.x / a.Hk : a.Hk, q = blockIdx.x / n, r = blockIdx.x % n;
+    hk = a.paged ? q : r;
+    return a.paged ? r : q;
+}
+
 // keys that query token i of the tile's sequence sees: [0, result)
 __device__ __forceinline__ int keys_seen(const AttnArgs& a, const RowTile& t, int i) {
     if (!a.causal) return t.nk;
@@ -240,7 +250,7 @@ inline int rows_tile_f32(int G, int64_t Tq, int B) {
 }
 
 // keys of a tile of the CUDA-core kernel: a block's Q, K, V and weights fit an SM three times (D = 64) or twice
-__host__ __device__ constexpr int simt_keys(int D) { return D == 64 ? 64 : 32; }
+__host__ __device__ constexpr int simt_keys(int D) { return D == 64 ? 64 : 48; }
 // query rows of a block of the tensor-core kernel, and such blocks on an SM
 __host__ __device__ constexpr int tc_rows(int D) { return D == 64 ? 128 : 256; }
 constexpr int tc_per_sm(int D) { return D == 64 ? 2 : 1; }

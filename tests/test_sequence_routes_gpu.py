@@ -2,6 +2,10 @@
 tensor cores, few rows, float32 - and at what is hard on each: non-finite values in unseen
 places, layouts, page sizes, scales from end to end of their range, many sequences, caches
 beyond 32-bit offsets, split keys.  Tolerances are those of test_sequence_gpu.py."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -280,6 +284,33 @@ def test_withheld_signal_times_out_and_later_calls_run(D, kind):
     vdm.vdm_attention_status()
     assert torch.equal(call(), want)
     vdm.vdm_attention_status()
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    """A fresh process whose first call of each operator is inside a capture."""
+    code = """
+import torch, neural_sdf_volume_b200 as vdm
+i32 = lambda x: torch.tensor(x, dtype=torch.int32, device='cuda')
+n = 1500
+q, k = torch.randn(n, 8, 128, device='cuda').bfloat16(), torch.randn(n, 2, 128, device='cuda').bfloat16()
+qf, kf, cu, one, ln, table = q.float(), k.float(), i32([0, n]), i32([0, 1]), i32([n]), i32([list(range(50))])
+cache, rope, pos, g1 = vdm.KVCache.create(64, 32, 2, 128, 'e4m3'), vdm.Rope.make(64), torch.arange(n, dtype=torch.int32, device='cuda'), torch.ones(128, device='cuda')
+torch.cuda.synchronize()
+for f in (lambda: vdm.vdm_qk_norm_rope(q, k, pos, rope, q_gain=g1)[0], lambda: vdm.vdm_cache_write(cache, k, k, cu, ln, table),
+          lambda: vdm.vdm_cache_read(cache, ln, table, cu, total=n)[0], lambda: vdm.vdm_attention_packed(q, k, k, cu),
+          lambda: vdm.vdm_attention_paged(q[:1], cache, one, ln, table), lambda: vdm.vdm_attention_packed(qf, kf, kf, cu)):
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o = f()
+    g.replay()
+    torch.cuda.synchronize()
+    w = f()
+    assert o is None or torch.equal(o, w)
+vdm.vdm_attention_status()
+print('captured')
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 def test_two_graphs_and_an_eager_call_at_once():
