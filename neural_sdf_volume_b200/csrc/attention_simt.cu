@@ -37,9 +37,9 @@ __global__ void __launch_bounds__(ST, D == 64 ? 3 : 2) attention_simt_kernel(con
     float* Vs = Ks + BK * LD;
     float* Ps = Vs + BK * LD;
     RowTile t;
-    int hk;
-    if (!find_tile(a, head_of(a, hk), BR, a.causal, t)) return;
-    const int split = blockIdx.y;
+    const BlockPlace place = place_of<PAGED>(a);
+    if (!find_tile(a, place.tile, BR, a.causal, t)) return;
+    const int hk = place.hk, split = place.split;
     const KvRows<TC, PAGED> kv{a, t, hk};
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int n_rows = min(BR, (int)((int64_t)t.nq * a.G - t.row0));
@@ -255,7 +255,7 @@ vdm_status launch(const AttnArgs& a, cudaStream_t s) {
     static std::atomic<uint64_t> ready{0};
     VDM_TRY(prepare_kernel(ready, reinterpret_cast<const void*>(kern), smem));
     const int64_t tiles = row_tiles(a.Tq, a.G, a.B, BR);
-    kern<<<dim3((unsigned)(tiles * a.Hk), a.splits), ST, smem, s>>>(a);
+    kern<<<tile_grid(a, tiles), ST, smem, s>>>(a);
     VDM_TRY(check_launch("attention_simt_kernel"));
     return a.splits > 1 ? launch_combine(a, sizeof(T) == 4 ? VDM_F32 : VDM_BF16, s) : VDM_OK;
 }

@@ -173,9 +173,9 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     Shared<NT>& sh = *reinterpret_cast<Shared<NT>*>(dyn_raw + C::TILES);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     RowTile t;
-    int hk;
-    if (!find_tile(a, head_of(a, hk), NT * BM, a.causal, t)) return;
-    const int split = blockIdx.y;
+    const BlockPlace place = place_of<SRC != kPacked>(a);
+    if (!find_tile(a, place.tile, NT * BM, a.causal, t)) return;
+    const int hk = place.hk, split = place.split;
     const int total_rows = t.nq * a.G;
     const uint32_t base = smem_u32(dyn_raw);
     const uint32_t s_ring = base + NT * C::QBYTES;
@@ -642,7 +642,7 @@ vdm_status launch(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& 
     static std::atomic<uint64_t> ready{0};
     VDM_TRY(prepare_kernel(ready, reinterpret_cast<const void*>(kern), smem_bytes<D>()));
     const int64_t tiles = row_tiles(a.Tq, a.G, a.B, tc_rows(D));
-    kern<<<dim3((unsigned)(tiles * a.Hk), a.splits), Cfg<D>::threads(SRC), smem_bytes<D>(), s>>>(mk, mv, a, tok_first);
+    kern<<<tile_grid(a, tiles), Cfg<D>::threads(SRC), smem_bytes<D>(), s>>>(mk, mv, a, tok_first);
     VDM_TRY(check_launch("attention_tc_kernel"));
     return a.splits > 1 ? launch_combine(a, VDM_BF16, s) : VDM_OK;
 }

@@ -185,8 +185,6 @@ vdm_status run_attention(const vdm_attention* at, AttnArgs& a, int64_t max_kv, c
     a.lse = lse;
     if ((int64_t)a.Tq * a.G > 0x7fffffffll)
         return fail(VDM_ERR_UNSUPPORTED, "attention: %lld query tokens of %d heads per group", (long long)a.Tq, a.G);
-    if (row_tiles(a.Tq, a.G, a.B, 1) * at->Hk > 0x7fffffffll * 64)
-        return fail(VDM_ERR_UNSUPPORTED, "attention: %lld query tokens of %d heads", (long long)a.Tq, at->Hq);
     size_t need = 0;
     VDM_TRY(vdm_attention_workspace_size(at, a.B, a.Tq, max_kv, &need));
     if (need && (!ws || ws_bytes < need))

@@ -129,14 +129,25 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int64_t idx, int M,
     return true;
 }
 
-// Key head and tile number of a block of grid x = tiles x heads.  Packed: the heads of a tile beside one
-// another, so that blocks start in the order of their lengths, whatever their head (packed_vecsets 111 us,
-// head after head 120; packed_prompts 356 and 368).  Paged: a head's tiles beside one another, since contexts
-// are long and a head's tiles then meet its keys in the cache (paged_chunk 218 us, the other way 228).
-__device__ __forceinline__ int64_t head_of(const AttnArgs& a, int& hk) {
-    const unsigned n = a.paged ? gridDim.x / a.Hk : a.Hk, q = blockIdx.x / n, r = blockIdx.x % n;
-    hk = a.paged ? q : r;
-    return a.paged ? r : q;
+// Grid of the large-tile kernels, and key head, tile number and split of a block of it.  Packed: the heads of
+// a tile beside one another, so that blocks start in the order of their lengths, whatever their head
+// (packed_vecsets 111 us, head after head 120; packed_prompts 356 and 368).  Paged: a head's tiles beside one
+// another, since contexts are long and a head's tiles then meet its keys in the cache (paged_chunk 217 us,
+// the other way 228).  The head is a coordinate of the grid: computed from one it cost 4 %.
+constexpr int64_t kTilesY = 65535;
+inline dim3 tile_grid(const AttnArgs& a, int64_t tiles) {
+    if (a.paged) return dim3((unsigned)tiles, a.Hk, a.splits);
+    return dim3(a.Hk, (unsigned)(tiles < kTilesY ? tiles : kTilesY), (unsigned)((tiles + kTilesY - 1) / kTilesY * a.splits));
+}
+struct BlockPlace {
+    int hk, split;
+    int64_t tile;
+};
+template <bool PAGED>
+__device__ __forceinline__ BlockPlace place_of(const AttnArgs& a) {
+    if (PAGED) return {(int)blockIdx.y, (int)blockIdx.z, blockIdx.x};
+    if (gridDim.z == a.splits) return {(int)blockIdx.x, (int)blockIdx.z, blockIdx.y};
+    return {(int)blockIdx.x, (int)(blockIdx.z % a.splits), blockIdx.y + kTilesY * (blockIdx.z / a.splits)};
 }
 
 // keys that query token i of the tile's sequence sees: [0, result)

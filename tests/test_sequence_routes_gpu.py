@@ -87,6 +87,16 @@ def test_packed_all_keys_of_minus_infinity(n, dtype):
     close(o, want, S.tolerance(np64(q), np64(k)[: n // 2], np64(v), want, 0.125, dtype)[0])
 
 
+def test_packed_more_row_tiles_than_a_grid_dimension():
+    """8.5 million queries of one sequence over 64 keys without a preference: every row is the mean of the values."""
+    n = 8_500_000
+    q, k, v = torch.ones(n, 1, 64, device="cuda", dtype=torch.bfloat16), torch.zeros(64, 1, 64, device="cuda", dtype=torch.bfloat16), randn(1, 64, 1, 64)
+    o = vdm.vdm_attention_packed(q, k, v, ints([0, n]), ints([0, 64]), causal=False)
+    vdm.vdm_attention_status()
+    assert torch.equal(o, o[:1].expand_as(o))
+    close(o[:1], np64(v).mean(0)[None], 2.0 ** -8 * np.abs(np64(v)).max())
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("n", [20, 1100])
 def test_layouts_give_the_same_result(dtype, n):
