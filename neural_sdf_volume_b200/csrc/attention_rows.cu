@@ -4,7 +4,7 @@
 //
 // A row is (token, query head of the group); a tile is up to 16 rows of one sequence and key
 // head.  The tile's keys are shared out over the warps of a cluster of blocks (and, beyond
-// 16 blocks, over grid z with partial results in the workspace): warp w takes steps w, w + n, ...
+// eight blocks, over grid z with partial results in the workspace): warp w takes steps w, w + n, ...
 // of KS keys.  Each warp keeps a ring of steps in shared memory of its own, filled by 16-byte
 // asynchronous copies (no barrier between warps until the end), and runs the softmax's running
 // maximum and sum on its keys alone:
@@ -29,6 +29,11 @@
 //
 // Masked keys: rows of V that no row of the tile sees are read as zeros.  Rows that
 // only its later queries see can bring 0 * NaN; see repair_row.
+//
+// Measured: 48 sequences of 300 to 16000 tokens, one query token each, 32/8 heads of 128, 8-bit (801 MB): 143 us,
+// 5.6 TB/s, 85 % of the copy rate; with queries as M and keys as N, half of each product empty, and the keys'
+// scales unpacked by every lane, 239 us.  One sequence of 700 tokens, 8 heads of 64: 6.2 us, which is loads that wait
+// for one another (offsets, page, keys: 1.1 + 1.0 + 0.7 us) and 2.1 us of joining.
 #include <type_traits>
 
 #include "attention_join.cuh"

@@ -45,9 +45,9 @@ __device__ __forceinline__ int row_exponent(float m) {
     return m == 0.f ? 0 : e < -100 ? -100 : e > 119 ? 119 : e;
 }
 
-// 8 elements as floats, and their largest magnitude (bits of a float; infinities and NaN among them stay)
-__device__ __forceinline__ uint32_t open8(const uint4 (&u)[1], float (&x)[8]) {
-    const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+// 16 bytes as floats, and their largest magnitude (bits of a float; infinities and NaN stay)
+__device__ __forceinline__ uint32_t open16(uint4 u, float (&x)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -56,28 +56,24 @@ __device__ __forceinline__ uint32_t open8(const uint4 (&u)[1], float (&x)[8]) {
     }
     return max(m << 16, m & 0xffff0000u);
 }
-__device__ __forceinline__ uint32_t open8(const uint4 (&u)[2], float (&x)[8]) {
+__device__ __forceinline__ uint32_t open16(uint4 u, float (&x)[4]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[4 * i + j] = __uint_as_float(w[j]);
-            m = max(m, w[j] & 0x7fffffffu);
-        }
-    }
+    for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(w[i]), m = max(m, w[i] & 0x7fffffffu);
     return m;
 }
 
+// As they are: a lane has 8 elements of a row.  E4M3: 16, so that a row's maximum takes fewer shuffles and codes leave
+// 16 bytes at a time.
 template <typename T, bool E4M3>
-__global__ void __launch_bounds__(CT, 20) cache_write_kernel(const __grid_constant__ CacheIo a) {
-    constexpr int W = (int)sizeof(T) / 2, U = 8 / W;   // 16-byte loads of 8 elements, pieces of 8 under way
+__global__ void __launch_bounds__(CT, 16) cache_write_kernel(const __grid_constant__ CacheIo a) {
+    constexpr int N = E4M3 ? 16 : 8, V = 16 / (int)sizeof(T), W = N / V, U = 8 / W;   // elements of a lane and of a load, loads, pieces under way
     const int lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * (CT / 32) + (threadIdx.x >> 5);
     if (t >= a.T) return;
-    const int lph = a.c.D / 8, hpw = 32 / lph, groups = (a.c.H + hpw - 1) / hpw;   // lanes of a head, heads of the warp
-    const int e0 = (lane % lph) * 8, sub = lane / lph;
+    const int lph = a.c.D / N, hpw = 32 / lph, groups = (a.c.H + hpw - 1) / hpw;   // lanes of a head, heads of the warp
+    const int e0 = (lane % lph) * N, sub = lane / lph;
     uint4 raw[U][W];
     auto load = [&](int v0) {   // v: group of heads, keys then values
 #pragma unroll
@@ -116,32 +112,37 @@ __global__ void __launch_bounds__(CT, 20) cache_write_kernel(const __grid_consta
                     for (int w = 0; w < W; ++w) reinterpret_cast<uint4*>(reinterpret_cast<T*>(dst) + r * a.c.D + e0)[w] = raw[u][w];
                 continue;
             }
-            float x[8];
-            uint32_t mb = open8(raw[u], x);
+            float x[W][V];
+            uint32_t mb = 0;
+#pragma unroll
+            for (int w = 0; w < W; ++w) mb = max(mb, open16(raw[u][w], x[w]));
             for (int o = 1; o < lph; o <<= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, o));
             if (__any_sync(0xffffffffu, mb >= 0x7f800000u)) {   // infinities become NaN, and neither counts
                 mb = 0;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (!isfinite(x[e])) x[e] = __uint_as_float(0x7fc00000u);
-                    else mb = max(mb, __float_as_uint(fabsf(x[e])));
-                }
+                for (int w = 0; w < W; ++w)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        if (!isfinite(x[w][e])) x[w][e] = __uint_as_float(0x7fc00000u);
+                        else mb = max(mb, __float_as_uint(fabsf(x[w][e])));
+                    }
                 for (int o = 1; o < lph; o <<= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, o));
             }
             const int e = row_exponent(__uint_as_float(mb));
             const uint64_t inv = ptx::f32x2(pow2i(-e), pow2i(-e));
-            uint32_t w[2];
+            uint32_t c[N / 4];
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
+            for (int p = 0; p < N / 4; ++p) {
+                const float* q = &x[4 * p / V][4 * p % V];
                 float y[4];
-                ptx::f32x2_split(ptx::mul_f32x2(ptx::f32x2(x[4 * p], x[4 * p + 1]), inv), y[0], y[1]);
-                ptx::f32x2_split(ptx::mul_f32x2(ptx::f32x2(x[4 * p + 2], x[4 * p + 3]), inv), y[2], y[3]);
+                ptx::f32x2_split(ptx::mul_f32x2(ptx::f32x2(q[0], q[1]), inv), y[0], y[1]);
+                ptx::f32x2_split(ptx::mul_f32x2(ptx::f32x2(q[2], q[3]), inv), y[2], y[3]);
                 const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
                 const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
-                w[p] = lo | (hi << 16);
+                c[p] = lo | (hi << 16);
             }
             if (on) {
-                *reinterpret_cast<uint2*>(dst + r * a.c.D + e0) = make_uint2(w[0], w[1]);
+                *reinterpret_cast<uint4*>(dst + r * a.c.D + e0) = make_uint4(c[0], c[1], c[2 % (N / 4)], c[3 % (N / 4)]);
                 if (e0 == 0) (side ? a.c.vs : a.c.ks)[r] = (uint8_t)(e + 127);
             }
         }

@@ -24,6 +24,9 @@ vdm_status attention_error_word(int** p) {
     return VDM_OK;
 }
 
+// tokens, positions and query rows: a tile beyond the last still counts in 32 bits
+constexpr int64_t kMost = 0x7fff0000ll;
+
 size_t dtype_size(vdm_dtype d) { return d == VDM_F32 ? 4 : 2; }
 bool al16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
@@ -54,7 +57,7 @@ vdm_status check_heads(const char* what, const vdm_heads* h, int64_t T, int H, i
 
 vdm_status check_count(const char* what, int64_t T, int B) {
     if (T < 0 || B < 0) return fail(VDM_ERR_INVALID_ARG, "%s: negative size (%lld tokens, %d sequences)", what, (long long)T, B);
-    if (T > 0x7fffffffll) return fail(VDM_ERR_UNSUPPORTED, "%s: %lld tokens do not fit in 32-bit offsets", what, (long long)T);
+    if (T > kMost) return fail(VDM_ERR_UNSUPPORTED, "%s: %lld tokens do not fit in 32-bit offsets", what, (long long)T);
     return VDM_OK;
 }
 
@@ -69,7 +72,7 @@ vdm_status check_cache(const vdm_kv_cache* c, const int32_t* table, int max_page
     while ((16 << shift) < c->page_size && shift < 4) ++shift;
     if ((16 << shift) != c->page_size)
         return fail(VDM_ERR_UNSUPPORTED, "cache: page_size = %d not in {16, 32, 64, 128, 256}", c->page_size);
-    if ((int64_t)max_pages * c->page_size > 0x7fffffffll)
+    if ((int64_t)max_pages * c->page_size > kMost)
         return fail(VDM_ERR_UNSUPPORTED, "cache: %d pages of %d tokens do not fit in 32-bit positions", max_pages, c->page_size);
     if (c->num_pages > 0) {
         if (!c->k || !c->v || !al16(c->k) || !al16(c->v))
@@ -183,7 +186,7 @@ vdm_status run_attention(const vdm_attention* at, AttnArgs& a, int64_t max_kv, c
     a.causal = at->causal;
     a.scale_log2 = at->scale * 1.44269504088896340736f;
     a.lse = lse;
-    if ((int64_t)a.Tq * a.G > 0x7fffffffll)
+    if ((int64_t)a.Tq * a.G > kMost)
         return fail(VDM_ERR_UNSUPPORTED, "attention: %lld query tokens of %d heads per group", (long long)a.Tq, a.G);
     size_t need = 0;
     VDM_TRY(vdm_attention_workspace_size(at, a.B, a.Tq, max_kv, &need));

@@ -130,10 +130,11 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int64_t idx, int M,
 }
 
 // Grid of the large-tile kernels, and key head, tile number and split of a block of it.  Packed: the heads of
-// a tile beside one another, so that blocks start in the order of their lengths, whatever their head
-// (packed_vecsets 111 us, head after head 120; packed_prompts 356 and 368).  Paged: a head's tiles beside one
-// another, since contexts are long and a head's tiles then meet its keys in the cache (paged_chunk 217 us,
-// the other way 228).  The head is a coordinate of the grid: computed from one it cost 4 %.
+// a tile beside one another, so that blocks start in the order of their lengths, whatever their head (six sets of
+// up to 4096 tokens, 8 heads of 64: 111 us, head after head 120; five prompts of up to 4096 tokens, 32/8 heads
+// of 128: 356 and 368).  Paged: a head's tiles beside one another, since contexts are long and a head's tiles
+// then meet its keys in the cache (512 new tokens after 15000, 32/8 heads of 128: 217 us, the other way 228).
+// The head is a coordinate of the grid: computed from one it cost 4 %.
 constexpr int64_t kTilesY = 65535;
 inline dim3 tile_grid(const AttnArgs& a, int64_t tiles) {
     if (a.paged) return dim3((unsigned)tiles, a.Hk, a.splits);

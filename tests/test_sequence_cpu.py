@@ -126,6 +126,7 @@ def test_cache_call_refusals():
     assert w(cu=None) == 1 and w(ln=None) == 1 and w(tab=None) == 1
     assert w(k=H(0)) == 1 and w(v=H(st=60)) == 1
     assert w(mp=1 << 28) == 2                                          # positions beyond 32 bits
+    assert w(mp=(1 << 27) - 1) == 2                                    # and so near that a tile would be
     assert w(T=0) == 0 and w(B=0, tab=None) == 0 and w(mp=0, tab=None) == 0
     assert lib.vdm_cache_read(cache(), 1, P, P, 4, None, 2, 4, H(), H(), None) == 1
     assert lib.vdm_cache_read(None, 1, P, P, 4, P, 2, 4, H(), H(), None) == 1
@@ -152,6 +153,7 @@ def test_attention_call_refusals():
     assert f(cq=None) == 1 and f(ck=None) == 1 and f(q=H(0)) == 1 and f(k=H(0)) == 1 and f(v=H(P + 1)) == 1
     assert f(o=H(0)) == 1 and f(o=H(st=0)) == 1 and f(k=H(st=0)) == 1
     assert f(Tq=-1) == 1 and f(Tk=-1) == 1 and f(B=-1) == 1 and f(Tq=1 << 31) == 2 and f(Tk=1 << 31) == 2
+    assert f(Tk=0x7fffffff) == 2 and f(Tq=0x7fffffff) == 2
     assert f(Tq=0) == 0 and f(B=0) == 0
     assert f(a=attn(Hq=64, Hk=1), q=H(st=4096), o=H(st=4096), Tq=1 << 26, B=1) == 2    # rows beyond 32 bits
     assert lib.vdm_attention_packed(None, H(), H(), H(), P, P, 2, 4, 4, H(), None, P, 1 << 40, None) == 1
