@@ -16,7 +16,9 @@
 namespace vdm {
 namespace {
 
-constexpr int CT = 64;   // small blocks, twenty on an SM: 47 and 76 us for the prompts and contexts of 200 and 460 MB, 128 threads without a bound 50 and 85
+// Small blocks, many on an SM.  Contexts of 460 MB read in 76 us with twenty (128 threads without a bound: 85); prompts
+// of 200 MB written in 47 us with twenty and 8 elements a lane, 36 with sixteen and 16.
+constexpr int CT = 64;
 
 // Sequence that owns token t (offsets ascending), by a whole warp; -1: none.
 __device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int64_t t) {
