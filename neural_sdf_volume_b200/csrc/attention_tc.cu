@@ -65,9 +65,10 @@ template <int D> struct Cfg {
     // warps that widen 8-bit tiles: a tile of D = 128 keeps seven busy
     static constexpr int WIDEN = NT == 1 ? 3 : 7;
     static constexpr int threads(int src) { return 128 * NT + (src == kPagedE4m3 ? 32 + 32 * WIDEN : 128); }
-    // registers a thread, out of 128 at launch (two CTAs of 256 threads, one of 512) or 168 (one of 384)
-    static constexpr int regs_softmax(int src) { return threads(src) == 384 ? 208 : 192; }
-    static constexpr int regs_other(int src) { return threads(src) == 384 ? 88 : 64; }
+    // registers a thread, out of 128 at launch (two CTAs of 256 threads, one of 512) or 168 (one of 384); widening
+    // warps take what keeps both sides from spilling
+    static constexpr int regs_softmax(int src) { return threads(src) == 384 ? 208 : src != kPagedE4m3 ? 192 : NT == 1 ? 176 : 184; }
+    static constexpr int regs_other(int src) { return threads(src) == 384 ? 88 : src != kPagedE4m3 ? 64 : NT == 1 ? 80 : 72; }
     static constexpr int QBYTES = BM * D * 2;        // one query tile
     static constexpr int SLOT = BN * D * 2;          // one key or value tile
     static constexpr int NS = D == 128 ? 5 : 6;      // slots beside the query tiles in 227 KB (113 KB)
@@ -539,22 +540,28 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     } else {
         // ------------------------------------------------------------ 8-bit tiles widened to bf16
         // A thread keeps one column of 16 codes and every ROWS-th row of a tile; a row of the next tile is asked
-        // for as soon as this tile's is widened.
+        // for as soon as this tile's is widened.  Pages are looked up a key tile ahead, lane i those of its keys
+        // 16 i .. 16 i + 15 (looked up right before its row, a warp waited for every lookup).
         constexpr int CH = D / 16, ROWS = 32 * C::WIDEN / CH, U = (BN + ROWS - 1) / ROWS;
         const int ct = tid - 32 * (MMA_WARP + 1), c = ct % CH, r0 = ct / CH;
         const int items = 2 * (jmax - jb);
+        const int32_t* table = a.c.table + (int64_t)t.b * a.c.max_pages;
         uint4 code[U];
         uint32_t scale[U];
+        auto look_up = [&](int j) {
+            const int key = j * BN + 16 * lane;
+            return lane < BN / 16 && key < t.nk ? table[key >> a.c.page_shift] : -1;
+        };
+        int page = look_up(jb), next = -1;
         auto ask = [&](int it, int u) {
             const int r = r0 + u * ROWS, key = (jb + (it >> 1)) * BN + r;
+            const int p = __shfl_sync(0xffffffffu, page, r >> 4);   // lanes behind the tile's hold -1
             code[u] = make_uint4(0u, 0u, 0u, 0u);
             scale[u] = 127;
-            if (it < items && r < BN && key < t.nk) {
-                const int64_t row = cache_row(a.c, t.b, hk, key);
-                if (row >= 0) {
-                    code[u] = *reinterpret_cast<const uint4*>((it & 1 ? a.c.v : a.c.k) + row * D + c * 16);
-                    scale[u] = (it & 1 ? a.c.vs : a.c.ks)[row];
-                }
+            if (it < items && key < t.nk && (uint32_t)p < (uint32_t)a.c.num_pages) {
+                const int64_t row = (((int64_t)p * a.c.H + hk) << a.c.page_shift) + (key & (a.c.page_size - 1));
+                code[u] = *reinterpret_cast<const uint4*>((it & 1 ? a.c.v : a.c.k) + row * D + c * 16);
+                scale[u] = (it & 1 ? a.c.vs : a.c.ks)[row];
             }
         };
 #pragma unroll
@@ -563,17 +570,19 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             const int slot = it % NS;
             if (it >= NS && !wait(&sh.empty[slot], ((it / NS) - 1) & 1, 9)) break;
             const uint32_t dst = s_ring + slot * C::SLOT;
+            if (it & 1) page = next;
+            else next = look_up(jb + (it >> 1) + 1);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int r = r0 + u * ROWS;
-                const float f = scale_of((uint8_t)scale[u]);
+                const uint32_t f = scale_bf16x2((uint8_t)scale[u]);
                 const uint32_t in[4] = {code[u].x, code[u].y, code[u].z, code[u].w};
                 uint32_t o[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float2 lo = e4m3x2_to_f((uint16_t)in[i]), hi = e4m3x2_to_f((uint16_t)(in[i] >> 16));
-                    o[2 * i] = pack_bf16(lo.x * f, lo.y * f);
-                    o[2 * i + 1] = pack_bf16(hi.x * f, hi.y * f);
+                    o[2 * i] = mul_bf16x2(pack_bf16(lo.x, lo.y), f);
+                    o[2 * i + 1] = mul_bf16x2(pack_bf16(hi.x, hi.y), f);
                 }
                 if (r < BN) {
                     st_v4(dst + tile_off(r, 2 * c), o[0], o[1], o[2], o[3]);

@@ -32,13 +32,6 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int64_t t) 
     return b >= 0 && t < cu[b + 1] ? b : -1;
 }
 
-// bf16 pairs times a power of two
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-
 // exponent of a row with largest finite magnitude m = f 2^E, f in [1/2, 1): 448 = 0.875 2^9, so that a
 // mantissa above 1.75 needs the next one
 __device__ __forceinline__ int row_exponent(float m) {

@@ -170,6 +170,16 @@ __device__ __forceinline__ float scale_of(uint8_t s) {
     return s ? __uint_as_float((uint32_t)s << 23) : __uint_as_float(0x00400000u);
 }
 
+// the same twice, as bf16
+__device__ __forceinline__ uint32_t scale_bf16x2(uint8_t s) { return (s ? (uint32_t)s << 7 : 0x40u) * 0x10001u; }
+
+// bf16 pairs times a power of two
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // two e4m3 codes as floats (exact)
 __device__ __forceinline__ float2 e4m3x2_to_f(uint16_t u) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(u, __NV_E4M3);
