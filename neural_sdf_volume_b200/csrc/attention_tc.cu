@@ -588,10 +588,11 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     st_v4(dst + tile_off(r, 2 * c), o[0], o[1], o[2], o[3]);
                     st_v4(dst + tile_off(r, 2 * c + 1), o[4], o[5], o[6], o[7]);
                 }
-                ask(it + 1, u);
             }
             fence_proxy_async();
             warp_arrive(&sh.full[slot]);
+#pragma unroll
+            for (int u = 0; u < U; ++u) ask(it + 1, u);
         }
       }
     }
