@@ -66,9 +66,9 @@ template <int D> struct Cfg {
     static constexpr int WIDEN = NT == 1 ? 3 : 7;
     static constexpr int threads(int src) { return 128 * NT + (src == kPagedE4m3 ? 32 + 32 * WIDEN : 128); }
     // registers a thread, out of 128 at launch (two CTAs of 256 threads, one of 512) or 168 (one of 384); widening
-    // warps take what keeps both sides from spilling
-    static constexpr int regs_softmax(int src) { return threads(src) == 384 ? 208 : src != kPagedE4m3 ? 192 : NT == 1 ? 176 : 184; }
-    static constexpr int regs_other(int src) { return threads(src) == 384 ? 88 : src != kPagedE4m3 ? 64 : NT == 1 ? 80 : 72; }
+    // warps want more (chunks at D = 64: 80 registers 330 us, 88 294, 96 298)
+    static constexpr int regs_softmax(int src) { return threads(src) == 384 ? 208 : src != kPagedE4m3 ? 192 : NT == 1 ? 168 : 184; }
+    static constexpr int regs_other(int src) { return threads(src) == 384 ? 88 : src != kPagedE4m3 ? 64 : NT == 1 ? 88 : 72; }
     static constexpr int QBYTES = BM * D * 2;        // one query tile
     static constexpr int SLOT = BN * D * 2;          // one key or value tile
     static constexpr int NS = D == 128 ? 5 : 6;      // slots beside the query tiles in 227 KB (113 KB)
@@ -539,9 +539,11 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         }
     } else {
         // ------------------------------------------------------------ 8-bit tiles widened to bf16
-        // A thread keeps one column of 16 codes and every ROWS-th row of a tile; a row of the next tile is asked
-        // for as soon as this tile's is widened.  Pages are looked up a key tile ahead, lane i those of its keys
-        // 16 i .. 16 i + 15 (looked up right before its row, a warp waited for every lookup).
+        // A thread keeps one column of 16 codes and every ROWS-th row of a tile; the next tile's are asked for once
+        // this one is announced, as the announcement's fence waits for loads too.  Pages are looked up a key tile
+        // ahead, lane i those of its keys 16 i .. 16 i + 15, and rows once for keys and values.  512 and 100 tokens
+        // over 15000 and 9000, 32/8 heads: 272 us at D = 128 (bf16 pages 217), 294 at 64; looked up right before its
+        // loads, these before the announcement: 384 and 504; codes by asynchronous copies through shared memory 318 and 438.
         constexpr int CH = D / 16, ROWS = 32 * C::WIDEN / CH, U = (BN + ROWS - 1) / ROWS;
         const int ct = tid - 32 * (MMA_WARP + 1), c = ct % CH, r0 = ct / CH;
         const int items = 2 * (jmax - jb);
@@ -552,26 +554,33 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             const int key = j * BN + 16 * lane;
             return lane < BN / 16 && key < t.nk ? table[key >> a.c.page_shift] : -1;
         };
-        int page = look_up(jb), next = -1;
-        auto ask = [&](int it, int u) {
-            const int r = r0 + u * ROWS, key = (jb + (it >> 1)) * BN + r;
-            const int p = __shfl_sync(0xffffffffu, page, r >> 4);   // lanes behind the tile's hold -1
-            code[u] = make_uint4(0u, 0u, 0u, 0u);
-            scale[u] = 127;
-            if (it < items && key < t.nk && (uint32_t)p < (uint32_t)a.c.num_pages) {
-                const int64_t row = (((int64_t)p * a.c.H + hk) << a.c.page_shift) + (key & (a.c.page_size - 1));
-                code[u] = *reinterpret_cast<const uint4*>((it & 1 ? a.c.v : a.c.k) + row * D + c * 16);
-                scale[u] = (it & 1 ? a.c.vs : a.c.ks)[row];
+        int page = look_up(jb);
+        int64_t row[U];   // of the key tile asked for, -1: none
+        auto rows = [&](int j) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int r = r0 + u * ROWS, key = j * BN + r;
+                const int p = __shfl_sync(0xffffffffu, page, r >> 4);   // lanes behind the tile's hold -1
+                row[u] = key < t.nk && (uint32_t)p < (uint32_t)a.c.num_pages
+                             ? (((int64_t)p * a.c.H + hk) << a.c.page_shift) + (key & (a.c.page_size - 1)) : -1;
             }
         };
+        auto ask = [&](int it, int u) {
+            code[u] = make_uint4(0u, 0u, 0u, 0u);
+            scale[u] = 127;
+            if (it < items && row[u] >= 0) {
+                code[u] = *reinterpret_cast<const uint4*>((it & 1 ? a.c.v : a.c.k) + row[u] * D + c * 16);
+                scale[u] = (it & 1 ? a.c.vs : a.c.ks)[row[u]];
+            }
+        };
+        rows(jb);
 #pragma unroll
         for (int u = 0; u < U; ++u) ask(0, u);
         for (int it = 0; it < items; ++it) {
             const int slot = it % NS;
             if (it >= NS && !wait(&sh.empty[slot], ((it / NS) - 1) & 1, 9)) break;
             const uint32_t dst = s_ring + slot * C::SLOT;
-            if (it & 1) page = next;
-            else next = look_up(jb + (it >> 1) + 1);
+            if (!(it & 1)) page = look_up(jb + (it >> 1) + 1);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int r = r0 + u * ROWS;
@@ -589,6 +598,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     st_v4(dst + tile_off(r, 2 * c + 1), o[4], o[5], o[6], o[7]);
                 }
             }
+            if (it & 1) rows(jb + (it >> 1) + 1);
             fence_proxy_async();
             warp_arrive(&sh.full[slot]);
 #pragma unroll
