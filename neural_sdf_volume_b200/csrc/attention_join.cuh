@@ -1,5 +1,5 @@
 // What the few-row attention kernels share: the joining of a tile's parts.  Every warp of the
-// tile's blocks has left its rows' maxima (log2 units), sums and unnormalised elements in shared
+// tile's blocks has left its rows' references (log2 units), sums and unnormalised elements in shared
 // memory; a row's parts are added in order - first the block's warps, then the blocks of the
 // cluster through distributed shared memory - so that a result does not depend on timing.
 #pragma once
@@ -35,19 +35,24 @@ __device__ __noinline__ float repair_row_apart(const AttnArgs& a, const RowTile&
     return repair_row<TC, D, PAGED>(a, t, hk, row, j0, j1, o);
 }
 
-// Parts of a lane's row (row = lane % 16) as factors of one sum: maxima pm, sums pl -> factors f, sum L; returns the
-// maximum, 0 for -inf.
-template <int P>
-__device__ __forceinline__ float join_factors(const float (&pm)[P], const float (&pl)[P], float (&f)[P], float& L) {
-    float M = pm[0];
+// Parts of a lane's row (row = lane % 16) as factors of one sum: references pm of their elements, their sums pl against
+// these - or, LOG, the log2 of the sums - -> factors f of the elements, the sum L; returns the reference that f refers to,
+// sum_ref the one of L (0 for -inf).
+template <bool LOG, int P>
+__device__ __forceinline__ float join_factors(const float (&pm)[P], const float (&pl)[P], float (&f)[P], float& L, float& sum_ref) {
+    auto top = [](const float (&x)[P]) {
+        float M = x[0];
 #pragma unroll
-    for (int p = 1; p < P; ++p) M = fmaxf(M, pm[p]);
-    const float ref = M == -INFINITY ? 0.f : M;
+        for (int p = 1; p < P; ++p) M = fmaxf(M, x[p]);
+        return M == -INFINITY ? 0.f : M;
+    };
+    const float ref = top(pm);
+    sum_ref = LOG ? top(pl) : ref;
     L = 0.f;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-        f[p] = pm[p] == -INFINITY && pl[p] == 0.f ? 0.f : exp2f(pm[p] - ref);   // no key: nothing
-        L = fmaf(f[p], pl[p], L);
+        f[p] = pm[p] == -INFINITY && pl[p] == (LOG ? -INFINITY : 0.f) ? 0.f : exp2f(pm[p] - ref);   // no key: nothing
+        L = LOG ? L + exp2f(pl[p] - sum_ref) : fmaf(f[p], pl[p], L);
     }
     return ref;
 }
@@ -61,8 +66,9 @@ __device__ __forceinline__ void add_part(float4& x, float f, const float4& y) {
 // finishes the rows b, b + n, ...: the others write their parts of them into its shared memory, so that one
 // barrier is enough (reading them there took a second one, before a block may leave, and 2 us in all).
 // Keys [j0, j1) are the ones of this split; a row that sees fewer of them and ends up not finite is computed
-// again (REPAIR).  ROWS: rows of a tile, at most.
-template <typename T, typename TC, int D, bool PAGED, int WARP, int ROWS, bool REPAIR>
+// again (REPAIR).  ROWS: rows of a tile, at most.  LOG: s_l holds the log2 of the sums, which may lie some 200 from the
+// elements' references.
+template <typename T, typename TC, int D, bool PAGED, int WARP, int ROWS, bool REPAIR, bool LOG>
 __device__ __forceinline__ void join_rows(const AttnArgs& a, const RowTile& t, int hk, int split, int rank, int cluster, int n_rows, int j0,
                                           int j1, float (&s_m)[RW][RM], float (&s_l)[RW][RM], uint32_t part) {
     constexpr int MAXC = 8;                          // blocks of a cluster, at most
@@ -73,12 +79,12 @@ __device__ __forceinline__ void join_rows(const AttnArgs& a, const RowTile& t, i
     const bool on = 4 * lane < D;
     const uint32_t at = part + 16 * lane;
     __syncthreads();
-    float fw[RW], L, ref;
+    float fw[RW], L, sum_ref, ref;
     {
         float pm[RW], pl[RW];
 #pragma unroll
         for (int w = 0; w < RW; ++w) pm[w] = s_m[w][mine], pl[w] = s_l[w][mine];
-        ref = join_factors(pm, pl, fw, L);
+        ref = join_factors<LOG>(pm, pl, fw, L, sum_ref);
     }
     auto warps_sum = [&](int row) {
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -103,7 +109,7 @@ __device__ __forceinline__ void join_rows(const AttnArgs& a, const RowTile& t, i
         if (warp == 0 && lane < n_rows) {   // no key: -inf and 0
             const int place = rank * own + mine / cluster;
             st_cluster_f32(ptx::mapa(ptx::smem_u32(&s_mi[place]), mine % cluster), L == 0.f ? -INFINITY : ref);
-            st_cluster_f32(ptx::mapa(ptx::smem_u32(&s_li[place]), mine % cluster), L);
+            st_cluster_f32(ptx::mapa(ptx::smem_u32(&s_li[place]), mine % cluster), LOG ? (L == 0.f ? -INFINITY : sum_ref + log2f(L)) : L);
         }
         ptx::cluster_sync();
     }
@@ -116,11 +122,11 @@ __device__ __forceinline__ void join_rows(const AttnArgs& a, const RowTile& t, i
         for (int k = 0; k < MAXC; ++k) {
             const bool there = k < cluster && mine < n_own;
             pm[k] = there ? s_mi[k * own + mine] : -INFINITY;
-            pl[k] = there ? s_li[k * own + mine] : 0.f;
+            pl[k] = there ? s_li[k * own + mine] : LOG ? -INFINITY : 0.f;
         }
-        ref = join_factors(pm, pl, fc, L);
+        ref = join_factors<LOG>(pm, pl, fc, L, sum_ref);
     }
-    const float inv = L == 0.f ? 0.f : 1.0f / L, lse2 = L == 0.f ? -INFINITY : ref + log2f(L);
+    const float lse2 = L == 0.f ? -INFINITY : sum_ref + log2f(L), inv = L == 0.f ? 0.f : LOG ? exp2f(ref - lse2) : 1.0f / L;
     const int rr = t.row0 + min(mine * cluster + rank, n_rows - 1), see = keys_seen(a, t, rr / a.G), h = hk * a.G + rr % a.G;
     const int64_t tok = t.q0 + rr / a.G, prow = ((int64_t)split * a.Tq + tok) * a.Hq + h;
     const bool parts = a.splits > 1;

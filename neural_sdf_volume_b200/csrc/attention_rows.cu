@@ -21,17 +21,24 @@
 // 8-bit codes are widened to fp16 (exact).  Q is scaled per row by a power of two so that
 // its largest element is in [2^14, 2^15): what of a bf16 row fp16 cannot hold lies below 2^-38 of
 // that.  A key's scale goes into its score.  A value's scale 2^e goes into the exponent of its weight,
-// w = 2^(s + e - M), with M the running maximum of s + e, and l sums w 2^-e: a row's largest product
-// w v sets the reference whatever the scales of its keys are.  w is rounded to fp16 at 2^12 times
-// its value: its relative precision is 2^-12 down to w = 2^-26, below that an error of 2^-37.
+// w = 2^(s + e - M), with M the running maximum of s + e: a row's largest product w v sets the
+// reference of the product whatever the scales of its keys are; a value row of zeros has no
+// product, so that its e (0, as written) must not set M and counts as -100.  w is rounded to fp16 at 2^12 times
+// its value: off by 2^-11 of itself at most down to w = 2^-26, below that by 2^-37.
+// The sum l has nothing to do with the values: it adds 2^(s - R), with R a reference of the scores.  While all value
+// exponents are within 24 of one E0, R = M - E0 - 12 and a term is w 2^(E0 - e); what is lost where w flushes to zero
+// lies below 2^-42 of the largest term.  A step with other exponents computes its terms from the scores, against an R of
+// their own (M and R may lie 219 apart, more than float32's exponents hold below one reference), and takes its largest
+// e as E0; while R stays more than 60 from M - E0 - 12, so do the steps after it.  Against a sum of w 2^-e alone, which lost
+// keys 138 below M, this costs 2 to 5 % (a second exponential in every step 8 to 34 %).
 // bf16 values: e = 0 and w is rounded to bf16.
 // The reference follows the maximum when that has grown by more than 2^3.
 //
 // Masked keys: rows of V that no row of the tile sees are read as zeros.  Rows that
 // only its later queries see can bring 0 * NaN; see repair_row.
 //
-// Measured: 48 sequences of 300 to 16000 tokens, one query token each, 32/8 heads of 128, 8-bit (801 MB): 143 us,
-// 5.6 TB/s, 85 % of the copy rate; with queries as M and keys as N, half of each product empty, and the keys'
+// Measured: 48 sequences of 300 to 16000 tokens, one query token each, 32/8 heads of 128, 8-bit (801 MB): 146 us,
+// 5.5 TB/s, 84 % of the copy rate; with queries as M and keys as N, half of each product empty, and the keys'
 // scales unpacked by every lane, 239 us.  One sequence of 700 tokens, 8 heads of 64: 6.2 us, which is loads that wait
 // for one another (offsets, page, keys: 1.1 + 1.0 + 0.7 us) and 2.1 us of joining.
 #include <type_traits>
@@ -109,6 +116,73 @@ __device__ __forceinline__ int swizzle_k(int r, int c) { return CH > 4 ? c ^ ((r
 template <int CH>
 __device__ __forceinline__ int swizzle_v(int r, int c) { return CH > 4 ? c ^ (((r >> 1) & 3) << 1) : c ^ (((r >> 1) & 1) << 1); }
 
+constexpr float kW0 = 12.0f;   // 8-bit values: fp16 weights are kept at 2^12 times their value, and sums against M - E0 - 12
+constexpr int kNear = 24;      // how far from E0 a step's value exponents may lie
+
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float over_keys(float x) {   // a row's keys are on the lanes of the same t4
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+
+// The sum's terms of a step whose value exponents are not all near E0, or one of whose value rows is zeros: from the
+// scores, against their own reference R.  Out of line, since few calls meet it and the others' loop is shorter without.
+template <int NQ> struct Apart {
+    float s[4][NQ][2];               // score + value exponent of the lane's keys 8 k + g; zero rows': with -100 for 0 when done
+    float m[NQ][2], l[NQ][2], mx[NQ][2];
+    float ev;                        // of the key `lane`, and whether its value row is zeros
+    bool none;
+    int e0;
+    bool far;
+};
+template <int NQ>
+__device__ __noinline__ void sum_apart(Apart<NQ>& x, float (&s_r)[RM]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+    const float now = x.none ? -100.0f : x.ev, was = (float)(x.e0 - 127);
+    const uint32_t top_e = __reduce_max_sync(0xffffffffu, x.none ? 0u : (uint32_t)(x.ev + 127.0f));
+    if (top_e) x.e0 = (int)top_e;
+    float R[NQ][2], by[NQ][2];
+    bool no = false;
+    for (int r = 0; r < NQ; ++r)
+        for (int j = 0; j < 2; ++j) {
+            float sc[4], top = -INFINITY, mx = -INFINITY;
+            for (int k = 0; k < 4; ++k) {
+                sc[k] = x.s[k][r][j] - __shfl_sync(0xffffffffu, x.ev, 8 * k + g);
+                top = fmaxf(top, sc[k]);
+                x.s[k][r][j] = sc[k] + __shfl_sync(0xffffffffu, now, 8 * k + g);
+                mx = fmaxf(mx, x.s[k][r][j]);
+            }
+            top = over_keys(top);
+            x.mx[r][j] = mx = over_keys(mx);
+            // the row's first keys set R, later ones raise it
+            const float m = x.m[r][j], R0 = x.far ? s_r[8 * r + 2 * t4 + j] : m - was - kW0;
+            const float R1 = m == -INFINITY ? (top == -INFINITY ? 0.f : top) : top > R0 + 16.0f ? top : R0;
+            float l = x.l[r][j];
+            if (l != 0.f) l *= ex2(R0 - R1);
+            for (int k = 0; k < 4; ++k) l += ex2(sc[k] - R1);
+            x.l[r][j] = l;
+            // against M - E0 - 12 again?
+            const float mn = fmaxf(m, mx);
+            R[r][j] = R1;
+            by[r][j] = mn == -INFINITY ? 0.f : R1 - (mn - (float)(x.e0 - 127) - kW0);
+            no = no || fabsf(by[r][j]) > 60.0f;
+        }
+    __syncwarp();
+    x.far = __any_sync(0xffffffffu, no);
+    for (int r = 0; r < NQ; ++r)
+        for (int j = 0; j < 2; ++j) {
+            if (x.far) {
+                if (g == 0) s_r[8 * r + 2 * t4 + j] = R[r][j];
+            } else if (x.l[r][j] != 0.f) x.l[r][j] *= ex2(by[r][j]);
+        }
+    __syncwarp();
+}
+
 // ROWS8: tiles have at most 8 rows, the other half of the matrix product's rows stays empty
 template <int D, int SRC, bool ROWS8>
 __global__ void __launch_bounds__(RW * 32, 3) attention_rows_kernel(const __grid_constant__ AttnArgs a, const int cluster) {
@@ -119,7 +193,7 @@ __global__ void __launch_bounds__(RW * 32, 3) attention_rows_kernel(const __grid
     constexpr int EC = E8 ? 16 : 8;                                   // elements of a chunk
     constexpr int KK = D / 16;
     extern __shared__ __align__(128) uint8_t dyn[];
-    __shared__ float s_m[RW][RM], s_l[RW][RM];
+    __shared__ float s_m[RW][RM], s_l[RW][RM], s_r[E8 ? RW : 1][RM];   // s_r: R where it is not M - E0
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     RowTile t;
     if (!find_tile(a, blockIdx.x, ROWS8 ? 8 : RM, a.causal, t)) return;   // the whole cluster alike
@@ -248,8 +322,9 @@ __global__ void __launch_bounds__(RW * 32, 3) attention_rows_kernel(const __grid
 #pragma unroll
         for (int i = 0; i < KK; ++i) o[i][r][0] = o[i][r][1] = o[i][r][2] = o[i][r][3] = 0.f;
     }
-    // fp16 weights are kept at 2^12 times their value; l, whose terms w 2^-e reach 2^(100 + 15), at 2^6
-    constexpr float W0 = E8 ? 12.0f : 0.0f, L0 = E8 ? 6.0f : 0.0f;
+    constexpr float W0 = E8 ? kW0 : 0.0f;
+    int e0 = -1;         // E0 as a scale byte; none yet
+    bool far = false;    // R is s_r's
 
     int slot = 0, fill = NS - 1;
     for (int step = first; step < s1; step += stride) {
@@ -260,6 +335,21 @@ __global__ void __launch_bounds__(RW * 32, 3) attention_rows_kernel(const __grid
         __syncwarp();
         const uint32_t bk = ring + slot * C::STAGE, bv = bk + KS * RB;
         slot = slot + 1 == NS ? 0 : slot + 1;
+
+        // 8-bit, a lane per key: scales; off: its value's exponent is not near E0
+        float kf = 0.f, ev_ = 0.f, inv_ = 0.f;
+        bool off = false;
+        if (E8) {
+            static_assert(!E8 || KS == 32, "a lane per key");
+            // value scales outside 2^-100 .. 2^119 are not valid; the zeros read for missing pages are among them
+            const uint32_t kb = lds_u8(bk + 2 * KS * RB + lane), vb = min(max(lds_u8(bk + 2 * KS * RB + KS + lane), 27u), 246u);
+            kf = scale_of((uint8_t)kb);
+            ev_ = __uint_as_float(0x4b000000u | vb) - (8388608.0f + 127.0f);   // 2^23 + vb as a float
+            const int some = (int)__shfl_sync(0xffffffffu, vb, 0);
+            e0 = e0 < 0 ? some : e0;
+            off = far || abs((int)vb - e0) > kNear;
+            inv_ = __uint_as_float((uint32_t)(127 + e0 - (int)vb) << 23);   // not used where one is off
+        }
 
         // scores: s[u][r][2 half + j] is key 16 u + 8 half + g, row 8 r + 2 t4 + j
         float s[U][NQ][4];
@@ -287,18 +377,12 @@ __global__ void __launch_bounds__(RW * 32, 3) attention_rows_kernel(const __grid
         // in log2 units, with the value scale's exponent added
         float inv[U][2];
         if (E8) {
-            static_assert(!E8 || KS == 32, "a lane per key");
-            // value scales outside 2^-100 .. 2^119 are not valid; the zeros read for missing pages are among them
-            const uint32_t kb = lds_u8(bk + 2 * KS * RB + lane), vb = min(max(lds_u8(bk + 2 * KS * RB + KS + lane), 27u), 246u);
-            const float f_ = scale_of((uint8_t)kb);
-            const float ev_ = __uint_as_float(0x4b000000u | vb) - (8388608.0f + 127.0f);   // 2^23 + vb as a float
-            const float inv_ = __uint_as_float((248u - vb) << 23);   // 2^(-exponent - L0)
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const int src = 16 * u + 8 * k + g;
-                    const float f = __shfl_sync(0xffffffffu, f_, src), ev = __shfl_sync(0xffffffffu, ev_, src);
+                    const float f = __shfl_sync(0xffffffffu, kf, src), ev = __shfl_sync(0xffffffffu, ev_, src);
                     inv[u][k] = __shfl_sync(0xffffffffu, inv_, src);
 #pragma unroll
                     for (int r = 0; r < NQ; ++r)
@@ -323,7 +407,7 @@ __global__ void __launch_bounds__(RW * 32, 3) attention_rows_kernel(const __grid
                         if (step * KS + 16 * u + 8 * (e >> 1) + g >= seen[r][e & 1]) s[u][r][e] = -INFINITY;
         }
         float mx[NQ][2];
-        bool raise = false;
+        bool raise = off, apart = false;   // apart: the step's sum from its scores
 #pragma unroll
         for (int r = 0; r < NQ; ++r)
 #pragma unroll
@@ -331,13 +415,45 @@ __global__ void __launch_bounds__(RW * 32, 3) attention_rows_kernel(const __grid
                 float x = fmaxf(s[0][r][j], s[0][r][2 + j]);
 #pragma unroll
                 for (int u = 1; u < U; ++u) x = fmax3(x, s[u][r][j], s[u][r][2 + j]);
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                mx[r][j] = x;
-                raise = raise || x > m[r][j] + 3.0f;
+                mx[r][j] = over_keys(x);
+                raise = raise || mx[r][j] > m[r][j] + 3.0f;
             }
         if (__any_sync(0xffffffffu, raise)) {
+            if (E8) {
+                // value rows of zeros (lane: key of the step); rarely more than a look at one chunk
+                auto zero = [&](int c) {
+                    const uint4 w = lds128(bv + lane * RB + c * 16);
+                    return ((w.x | w.y | w.z | w.w) & 0x7f7f7f7fu) == 0u;
+                };
+                bool none = zero(lane % CH);
+                if (__builtin_expect(__any_sync(0xffffffffu, none), 0)) {
+                    for (int c = 0; c < CH; ++c) none = none && zero(c);
+                    none = none && step * KS + lane < most;
+                }
+                apart = __any_sync(0xffffffffu, off || none);
+                if (__builtin_expect(apart, 0)) {
+                    Apart<NQ> x;
+#pragma unroll
+                    for (int r = 0; r < NQ; ++r)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            x.m[r][j] = m[r][j], x.l[r][j] = l[r][j];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) x.s[k][r][j] = s[k >> 1][r][2 * (k & 1) + j];
+                        }
+                    x.ev = ev_, x.none = none, x.e0 = e0, x.far = far;
+                    sum_apart(x, s_r[warp % (E8 ? RW : 1)]);
+                    e0 = x.e0, far = x.far;
+#pragma unroll
+                    for (int r = 0; r < NQ; ++r)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            l[r][j] = x.l[r][j], mx[r][j] = x.mx[r][j];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) s[k >> 1][r][2 * (k & 1) + j] = x.s[k][r][j];
+                        }
+                }
+            }
 #pragma unroll
             for (int r = 0; r < NQ; ++r)
 #pragma unroll
@@ -345,7 +461,7 @@ __global__ void __launch_bounds__(RW * 32, 3) attention_rows_kernel(const __grid
                     const float mn = fmaxf(m[r][j], mx[r][j]);
                     const float f = mn == -INFINITY ? 1.0f : exp2f(m[r][j] - mn);
                     m[r][j] = mn;
-                    l[r][j] *= f;
+                    if (!E8 || !apart) l[r][j] *= f;
 #pragma unroll
                     for (int i = 0; i < KK; ++i) o[i][r][j] *= f, o[i][r][2 + j] *= f;
                 }
@@ -353,16 +469,19 @@ __global__ void __launch_bounds__(RW * 32, 3) attention_rows_kernel(const __grid
         uint32_t p[U][NQ][2];   // weights of keys 16 u + 8 half + 2 t4 + {0, 1}, row 8 r + g
 #pragma unroll
         for (int r = 0; r < NQ; ++r) {
+            float sum0 = E8 ? 0.f : l[r][0], sum1 = E8 ? 0.f : l[r][1];
             const float ref0 = (m[r][0] == -INFINITY ? 0.f : m[r][0]) - W0, ref1 = (m[r][1] == -INFINITY ? 0.f : m[r][1]) - W0;
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const float w0 = ex2(s[u][r][2 * k] - ref0), w1 = ex2(s[u][r][2 * k + 1] - ref1);
-                    l[r][0] = E8 ? fmaf(w0, inv[u][k], l[r][0]) : l[r][0] + w0;
-                    l[r][1] = E8 ? fmaf(w1, inv[u][k], l[r][1]) : l[r][1] + w1;
+                    sum0 = E8 ? fmaf(w0, inv[u][k], sum0) : sum0 + w0;
+                    sum1 = E8 ? fmaf(w1, inv[u][k], sum1) : sum1 + w1;
                     p[u][r][k] = transpose8(E8 ? pack_f16(w0, w1) : pack_bf16(w0, w1));
                 }
+            if (!E8) l[r][0] = sum0, l[r][1] = sum1;
+            else if (!apart) l[r][0] += sum0, l[r][1] += sum1;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -407,16 +526,17 @@ __global__ void __launch_bounds__(RW * 32, 3) attention_rows_kernel(const __grid
     __syncwarp();
 
     // the warp's rows into its ring
-    const float w0 = pow2i(-(int)W0), l0 = pow2i((int)(L0 - W0));
+    const float w0 = pow2i(-(int)W0);
 #pragma unroll
     for (int r = 0; r < NQ; ++r)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int row = 8 * r + 2 * t4 + j;
-            float x = l[r][j] * l0;
+            float x = l[r][j];
             x += __shfl_xor_sync(0xffffffffu, x, 4);
             x += __shfl_xor_sync(0xffffffffu, x, 8);
             x += __shfl_xor_sync(0xffffffffu, x, 16);
+            if (E8) x = lg2(x) + (far ? s_r[warp % (E8 ? RW : 1)][row] : m[r][j] - (float)(e0 - 127) - W0);   // -inf of a sum of 0
             if (g == 0) s_m[warp][row] = m[r][j], s_l[warp][row] = x;
 #pragma unroll
             for (int i = 0; i < KK; ++i) {
@@ -425,7 +545,7 @@ __global__ void __launch_bounds__(RW * 32, 3) attention_rows_kernel(const __grid
                 asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(ring + (row * D + d) * 4), "f"(o[i][r][j] * w0), "f"(o[i][r][2 + j] * w0) : "memory");
             }
         }
-    join_rows<__nv_bfloat16, typename std::conditional<E8, uint8_t, __nv_bfloat16>::type, D, PAGED, C::WARP, ROWS8 ? 8 : 16, true>(
+    join_rows<__nv_bfloat16, typename std::conditional<E8, uint8_t, __nv_bfloat16>::type, D, PAGED, C::WARP, ROWS8 ? 8 : 16, true, E8>(
         a, t, hk, split, rank, cluster, n_rows, s0 * KS, min(s1 * KS, most), s_m, s_l, smem_u32(dyn));
 }
 

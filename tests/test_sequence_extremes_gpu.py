@@ -1,0 +1,103 @@
+"""Token-sequence operators on the GPU at the far ends of what their contract allows.
+Tolerances are those of test_sequence_gpu.py and test_sequence_routes_gpu.py; what is added stands at its place."""
+import numpy as np
+import pytest
+import torch
+
+import neural_sdf_volume_b200 as vdm
+import test_sequence_gpu as S
+from oracle import sequence as OS
+from test_sequence_gpu import U, close, ints, np64, offsets, randn
+from test_sequence_routes_gpu import weighted_tolerance
+
+pytestmark = pytest.mark.gpu
+
+
+# ----------------------------------------------------------------- value scales of an 8-bit cache
+
+def scaled(H, D, page, total, sv, seed=20, zero=()):
+    """A cache whose value rows have the scale bytes sv [tokens, H] (one sequence); the rows `zero` are zeros as written."""
+    c = S.Cached("e4m3", H, D, page, [total], seed=seed)
+    c.cache.k_scale.fill_(117)
+    for p in range(total):
+        c.cache.v_scale[c.tab[0, p // page], :, p % page] = torch.from_numpy(np.asarray(sv[p], np.uint8)).cuda()
+    for p in zero:
+        c.cache.v[c.tab[0, p // page], :, p % page] = 0
+        c.cache.v_scale[c.tab[0, p // page], :, p % page] = 127
+    c.rows["k"], c.rows["v"] = (OS.dequantise(t.cpu().numpy(), s.cpu().numpy()) for t, s in
+                                ((c.cache.k, c.cache.k_scale), (c.cache.v, c.cache.v_scale)))
+    return c
+
+
+def check_scaled(c, q, new=1, scale=None):
+    """Weights are fp16 at 2^12 times their share of 2^M, M at most the largest of score + value exponent: a rounding moves
+    a weight by 2^-11 of itself, or by 2^-37 of 2^M where that is more; codes are at most 448.  M, up to 220 beside the
+    score, is rounded once a part, and so is a score + value exponent that a sum's term is taken back from: factors of
+    1 + 220 ln 2 u of a weight and 1 + (2 * 120 + 2 |score|) ln 2 u of a term, the second's |score| in d."""
+    sc = q.shape[-1] ** -0.5 if scale is None else scale
+    k, v = c.sequence("k", 0), c.sequence("v", 0)
+    got, lse = vdm.vdm_attention_paged(q, c.cache, offsets([new]), c.kv_len, c.table, want_lse=True, scale=sc)
+    want, wl = OS.attention(np64(q), k, v, True, sc)
+    G = q.shape[1] // k.shape[1]
+    e = np.stack([c.cache.v_scale[c.tab[0, p // c.page], :, p % c.page].cpu().numpy() for p in range(len(k))]).astype(float) - 127
+    e[(v == 0).all(-1)] = -100
+    n = len(k)
+    for i in range(new):
+        m = n - new + i + 1
+        tol = weighted_tolerance(np64(q)[i:i + 1], k[:m], v[:m], sc, 2.0 ** -11 + 160 * U)
+        s = np.einsum("hd,khd->kh", np64(q)[i], np.repeat(k[:m], G, 1)) * sc
+        top = np.exp(s + np.repeat(e[:m], G, 1) * np.log(2) - wl[i]).max(0)          # [Hq], 2^M over the row's sum
+        close(got[i:i + 1], want[i:i + 1], tol + m * 448 * 2.0 ** -37 * top[None, :, None], f"row {i}")
+    d = (q.shape[-1] + 8) * U * sc * np.einsum("qhd,khd->qhk", np.abs(np64(q)), np.abs(np.repeat(k, G, 1))).max()
+    close(lse, wl, 2 * d + 170 * U + 2.0 ** -20 + (n + 16) * U + 4 * U * np.abs(np.where(np.isfinite(wl), wl, 0)), "lse")
+    return got, lse
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("a, b", [(27, 246), (246, 27), (57, 197), (27, 27), (246, 246)])
+@pytest.mark.parametrize("ahead", [0.0, 8.0, -8.0])
+def test_two_keys_at_both_ends_of_the_value_scales(D, a, b, ahead):
+    """Both count in the sum, whatever their values' scales are: equal scores, or either key ahead."""
+    c = scaled(2, D, 16, 2, [[a, a], [b, b]])
+    c.cache.k.zero_()
+    c.cache.k[c.tab[0, 0], :, 0, 0] = 0x38                           # 1.0, at scale 2^-10
+    c.rows["k"] = OS.dequantise(c.cache.k.cpu().numpy(), c.cache.k_scale.cpu().numpy())
+    q = torch.zeros(1, 8, D, device="cuda", dtype=torch.bfloat16)
+    q[..., 0] = ahead * 2.0 ** 10
+    got, lse = check_scaled(c, q, scale=1.0)
+    if ahead == 0.0:
+        close(lse, np.full((1, 8), np.log(2)), 2.0 ** -20)
+
+
+@pytest.mark.parametrize("D, Hq, Hk", [(64, 8, 2), (128, 8, 2), (128, 16, 1)])
+@pytest.mark.parametrize("total, new", [(33, 1), (900, 1), (900, 5), (20001, 1)])     # a step, warps, a cluster's rows, parts
+def test_value_scales_over_their_whole_range(D, Hq, Hk, total, new):
+    sv = np.random.default_rng(total).integers(27, 245, (total, Hk))
+    c = scaled(Hk, D, 64, total, sv)
+    q = randn(21, new, Hq, D)
+    _, lse = check_scaled(c, q, new)
+    c.cache.v_scale.fill_(127)                                       # the sums have nothing to do with the values
+    _, near = vdm.vdm_attention_paged(q, c.cache, offsets([new]), c.kv_len, c.table, want_lse=True)
+    close(lse, np64(near), (2 * 170 + 2 * (total + 16)) * U + 2.0 ** -19 + 2 * U * np.abs(np64(near)).max())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("e", [-45, -60, -95])
+@pytest.mark.parametrize("zero", [[0], list(range(40)), [450], list(range(0, 900, 2))])
+def test_zero_value_rows_beside_small_ones(D, e, zero):
+    """A row of zeros has the scale 2^0 whatever its neighbours' are; it must not push their weights below fp16."""
+    sv = np.full((900, 2), 127 + e)
+    check_scaled(scaled(2, D, 16, 900, sv, zero=zero), randn(22, 1, 8, D))
+
+
+def test_sums_when_scores_rise_and_fall_by_hundreds():
+    """Scores from far below to far above the first keys': the reference of the sum follows."""
+    for order in (1, -1):
+        c = scaled(1, 64, 16, 600, np.random.default_rng(3).integers(60, 190, (600, 1)))
+        c.cache.k.zero_()
+        for p in range(600):
+            c.cache.k[c.tab[0, p // 16], 0, p % 16, 0] = int(OS.e4m3_encode(float((p - 300) * order) / 1.5))
+        c.rows["k"] = OS.dequantise(c.cache.k.cpu().numpy(), c.cache.k_scale.cpu().numpy())
+        q = torch.zeros(1, 4, 64, device="cuda", dtype=torch.bfloat16)
+        q[0, :, 0] = torch.tensor([2.0 ** 10, 2.0 ** 11, -2.0 ** 11, 1.0])
+        check_scaled(c, q, scale=1.0)
