@@ -29,10 +29,20 @@ __device__ __forceinline__ void st_cluster_f4(uint32_t a, float4 v) {
 __device__ __forceinline__ void cluster_started() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// repair_row out of line: the few-row kernels run their code once, and what they do not run is better elsewhere
+// What a row's four elements x get of the non-finite values of keys [j0, j1), which the product left out (see odd_only).  Out of
+// line, with arguments that need no place in memory: the few-row kernels run their code once, and what they do not run is
+// better elsewhere (by references: 3 us of 44, four tokens each over 2000 to 8000).
 template <typename TC, int D, bool PAGED>
-__device__ __noinline__ float repair_row_apart(const AttnArgs& a, const RowTile& t, int hk, int row, int j0, int j1, float4& o) {
-    return repair_row<TC, D, PAGED>(a, t, hk, row, j0, j1, o);
+__device__ __noinline__ float4 add_odd(const AttnArgs* a, int b, int64_t k0, int hk, int j0, int j1, float4 x) {
+    const int d = 4 * (threadIdx.x & 31);
+    RowTile t;
+    t.b = b, t.k0 = k0;
+    const KvRows<TC, PAGED> kv{*a, t, hk};
+    for (int j = j0; j < j1 && d < D; ++j) {
+        const float4 v = kv.get(true, j, d);
+        x.x += odd_only(v.x), x.y += odd_only(v.y), x.z += odd_only(v.z), x.w += odd_only(v.w);
+    }
+    return x;
 }
 
 // Parts of a lane's row (row = lane % 16) as factors of one sum: references pm of their elements, their sums pl against
@@ -65,20 +75,21 @@ __device__ __forceinline__ void add_part(float4& x, float f, const float4& y) {
 // computed for all rows at once, a lane each; then a warp adds up its rows' elements.  In a cluster block b
 // finishes the rows b, b + n, ...: the others write their parts of them into its shared memory, so that one
 // barrier is enough (reading them there took a second one, before a block may leave, and 2 us in all).
-// Keys [j0, j1) are the ones of this split; a row that sees fewer of them and ends up not finite is computed
-// again (REPAIR).  ROWS: rows of a tile, at most.  LOG: s_l holds the log2 of the sums, which may lie some 200 from the
+// CLEAN: the values of keys [j0, j1) have lost their non-finite elements before the product, if a warp says so in s_odd;
+// they are added here to the rows that see them.  ROWS: rows of a tile, at most.  LOG: s_l holds the log2 of the sums, which may lie some 200 from the
 // elements' references.
-template <typename T, typename TC, int D, bool PAGED, int WARP, int ROWS, bool REPAIR, bool LOG>
+template <typename T, typename TC, int D, bool PAGED, int WARP, int ROWS, bool CLEAN, bool LOG>
 __device__ __forceinline__ void join_rows(const AttnArgs& a, const RowTile& t, int hk, int split, int rank, int cluster, int n_rows, int j0,
-                                          int j1, float (&s_m)[RW][RM], float (&s_l)[RW][RM], uint32_t part) {
+                                          int j1, float (&s_m)[RW][RM], float (&s_l)[RW][RM], const int* s_odd, uint32_t part) {
     constexpr int MAXC = 8;                          // blocks of a cluster, at most
     constexpr int TAKE = ROWS > MAXC ? ROWS : MAXC;  // rows that come in: a row of every block for each of its own
     __shared__ __align__(16) float s_in[TAKE][D];
-    __shared__ float s_mi[TAKE], s_li[TAKE];
+    __shared__ float s_mi[TAKE], s_li[TAKE], s_oi[MAXC];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mine = lane & (RM - 1);
     const bool on = 4 * lane < D;
     const uint32_t at = part + 16 * lane;
     __syncthreads();
+    bool odd = CLEAN && j0 < j1 && (s_odd[0] | s_odd[1] | s_odd[2] | s_odd[3]);
     float fw[RW], L, sum_ref, ref;
     {
         float pm[RW], pl[RW];
@@ -111,7 +122,10 @@ __device__ __forceinline__ void join_rows(const AttnArgs& a, const RowTile& t, i
             st_cluster_f32(ptx::mapa(ptx::smem_u32(&s_mi[place]), mine % cluster), L == 0.f ? -INFINITY : ref);
             st_cluster_f32(ptx::mapa(ptx::smem_u32(&s_li[place]), mine % cluster), LOG ? (L == 0.f ? -INFINITY : sum_ref + log2f(L)) : L);
         }
+        if (CLEAN && j0 < j1 && warp == 1 && lane < cluster) st_cluster_f32(ptx::mapa(ptx::smem_u32(&s_oi[rank]), lane), odd ? 1.0f : 0.f);
         ptx::cluster_sync();
+        if (CLEAN && j0 < j1)
+            for (int k = 0; k < cluster; ++k) odd = odd || s_oi[k] != 0.f;
     }
     // from here a lane's row is the mine-th of the block's own (all rows without a cluster)
     const int n_own = cluster == 1 ? n_rows : (n_rows - rank + cluster - 1) / cluster;
@@ -149,10 +163,9 @@ __device__ __forceinline__ void join_rows(const AttnArgs& a, const RowTile& t, i
         const float i = __shfl_sync(0xffffffffu, inv, row);
         x.x *= i, x.y *= i, x.z *= i, x.w *= i;
         char* const p = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), row));
-        if (REPAIR) {
+        if (CLEAN && odd) {
             const int end = min(__shfl_sync(0xffffffffu, see, row), j1);
-            const bool bad = !(fabsf(x.x) < INFINITY && fabsf(x.y) < INFINITY && fabsf(x.z) < INFINITY && fabsf(x.w) < INFINITY);
-            if (end < j1 && __any_sync(0xffffffffu, bad)) repair_row_apart<TC, D, PAGED>(a, t, hk, t.row0 + row * cluster + rank, j0, end, x);
+            if (__shfl_sync(0xffffffffu, L, row) != 0.f) x = add_odd<TC, D, PAGED>(&a, t.b, t.k0, hk, j0, end, x);
         }
         if (on) {
             if (parts) store4(reinterpret_cast<float*>(p) + 4 * lane, x);

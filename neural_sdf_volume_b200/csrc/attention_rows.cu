@@ -35,7 +35,7 @@
 // The reference follows the maximum when that has grown by more than 2^3.
 //
 // Masked keys: rows of V that no row of the tile sees are read as zeros.  Rows that
-// only its later queries see can bring 0 * NaN; see repair_row.
+// only its later queries see lose their non-finite elements in shared memory; see odd_only.
 //
 // Measured: 48 sequences of 300 to 16000 tokens, one query token each, 32/8 heads of 128, 8-bit (801 MB): 146 us,
 // 5.5 TB/s, 84 % of the copy rate; with queries as M and keys as N, half of each product empty, and the keys'
@@ -130,8 +130,25 @@ __device__ __forceinline__ float over_keys(float x) {   // a row's keys are on t
     return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
 }
 
+// Non-finite elements of the value rows [r0, r1) of a step become zeros; *s_odd says that there were some.  Out of line, as what follows: few
+// calls meet it, and the others' loop is shorter without.
+template <bool E8, int CH>
+__device__ __noinline__ void make_finite(uint32_t bv, int r0, int r1, int* s_odd) {
+    bool odd = false;
+#pragma unroll 1
+    for (int x = r0 * CH + (threadIdx.x & 31); x < r1 * CH; x += 32) {
+        uint4 v = lds128(bv + x * 16);
+        if (!any_odd<E8>(v)) continue;
+        odd = true;
+        v = without_odd<E8>(v);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(bv + x * 16), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+    }
+    if (odd) *s_odd = 1;
+    __syncwarp();
+}
+
 // The sum's terms of a step whose value exponents are not all near E0, or one of whose value rows is zeros: from the
-// scores, against their own reference R.  Out of line, since few calls meet it and the others' loop is shorter without.
+// scores, against their own reference R.
 template <int NQ> struct Apart {
     float s[4][NQ][2];               // score + value exponent of the lane's keys 8 k + g; zero rows': with -100 for 0 when done
     float m[NQ][2], l[NQ][2], mx[NQ][2];
@@ -194,6 +211,7 @@ __global__ void __launch_bounds__(RW * 32, 3) attention_rows_kernel(const __grid
     constexpr int KK = D / 16;
     extern __shared__ __align__(128) uint8_t dyn[];
     __shared__ float s_m[RW][RM], s_l[RW][RM], s_r[E8 ? RW : 1][RM];   // s_r: R where it is not M - E0
+    __shared__ int s_odd[RW];   // whether the warp has made values finite
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     RowTile t;
     if (!find_tile(a, blockIdx.x, ROWS8 ? 8 : RM, a.causal, t)) return;   // the whole cluster alike
@@ -323,6 +341,8 @@ __global__ void __launch_bounds__(RW * 32, 3) attention_rows_kernel(const __grid
         for (int i = 0; i < KK; ++i) o[i][r][0] = o[i][r][1] = o[i][r][2] = o[i][r][3] = 0.f;
     }
     constexpr float W0 = E8 ? kW0 : 0.0f;
+    if (lane == 0) s_odd[warp] = 0;
+    __syncwarp();
     int e0 = -1;         // E0 as a scale byte; none yet
     bool far = false;    // R is s_r's
 
@@ -335,6 +355,9 @@ __global__ void __launch_bounds__(RW * 32, 3) attention_rows_kernel(const __grid
         __syncwarp();
         const uint32_t bk = ring + slot * C::STAGE, bv = bk + KS * RB;
         slot = slot + 1 == NS ? 0 : slot + 1;
+
+        if (__builtin_expect(all_see < most && (step + 1) * KS > all_see, 0))   // values that not all rows see
+            make_finite<E8, CH>(bv, max(0, all_see - step * KS), min(KS, most - step * KS), &s_odd[warp]);
 
         // 8-bit, a lane per key: scales; off: its value's exponent is not near E0
         float kf = 0.f, ev_ = 0.f, inv_ = 0.f;
@@ -546,7 +569,7 @@ __global__ void __launch_bounds__(RW * 32, 3) attention_rows_kernel(const __grid
             }
         }
     join_rows<__nv_bfloat16, typename std::conditional<E8, uint8_t, __nv_bfloat16>::type, D, PAGED, C::WARP, ROWS8 ? 8 : 16, true, E8>(
-        a, t, hk, split, rank, cluster, n_rows, s0 * KS, min(s1 * KS, most), s_m, s_l, smem_u32(dyn));
+        a, t, hk, split, rank, cluster, n_rows, max(s0 * KS, all_see), min(s1 * KS, most), s_m, s_l, s_odd, smem_u32(dyn));
 }
 
 template <int D, int SRC, bool ROWS8>

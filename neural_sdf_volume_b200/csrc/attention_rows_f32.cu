@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(RW * 32) attention_rows_f32_kernel(const __gri
 #pragma unroll
             for (int i = 0; i < NI; ++i) *reinterpret_cast<float4*>(&s_part[warp][r][dim(i)]) = o[r][i];
     }
-    join_rows<float, TC, D, PAGED, WARP, R, false, false>(a, t, hk, split, rank, cluster, n_rows, 0, 0, s_m, s_l, ptx::smem_u32(&s_part[0][0][0]));
+    join_rows<float, TC, D, PAGED, WARP, R, false, false>(a, t, hk, split, rank, cluster, n_rows, 0, 0, s_m, s_l, nullptr, ptx::smem_u32(&s_part[0][0][0]));
 }
 
 template <typename TC, int D, bool PAGED, int R>

@@ -14,6 +14,7 @@
 //                        tensor cores work on the other's (D = 64: on the other CTA's);
 //   warp 4 NT + 1        TMA loads of K and V tiles into a ring of slots (packed: one box of 128
 //                        tokens per 64 columns; paged: one box per page);
+//   warps 4 NT + 2, 3    masked values made finite, in the last key tiles of causal calls;
 //   warps from 4 NT + 1  (8-bit cache) instead read codes from global memory, widen them to bf16 -
 //                        exact: a code times a power of two - and write the ring's slots.
 // The maximum that the exponents refer to follows the running maximum only when that has
@@ -35,10 +36,9 @@
 // (a 128 x 64 x 16 MMA takes as long as a 128 x 128 x 16 one).
 //
 // Masked keys: a key that a row does not see has weight 0.  V rows behind the sequence's end
-// are zeroed in shared memory (0 * NaN would reach every row); V rows inside the sequence that
-// only later queries see can still bring 0 * NaN or 0 * inf, so that a row which ends up not
-// finite while keys of its tiles were masked is computed again, over its own keys alone
-// (repair_row, one warp per row; never taken with finite values).
+// are zeroed in shared memory (0 * NaN would reach every row).  V rows inside the sequence that
+// not all rows of the CTA see lose their non-finite elements there, by the two warps that are idle otherwise (8-bit: while they
+// are widened), and the rows that do see such an element get it at the end: see odd_only.
 //
 // Every wait is bounded; on expiry the kernel sets the error word, winds down and frees TMEM.
 #include <cuda.h>
@@ -80,9 +80,11 @@ template <int D> struct Cfg {
 
 // behind the tiles
 template <int NT> struct Shared {
-    uint64_t q_full, full[8], empty[8], s_full[NT], s_read[NT], p_half[NT], p_full[NT], pv_done[NT];
+    uint64_t q_full, full[8], empty[8], s_full[NT], s_read[NT], p_half[NT], p_full[NT], pv_done[NT], look[8], clean[8];
     uint32_t tmem;
-    int abort;
+    int abort, odd;                      // odd: a value has been made finite
+    int odd_hk, odd_b, odd_from, odd_to;   // then wanted: key head, sequence and keys that this may be true of
+    long long odd_k0;
 };
 template <int D> constexpr int smem_bytes() { return Cfg<D>::TILES + (int)sizeof(Shared<Cfg<D>::NT>); }
 static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 115712, "shared memory of an SM");
@@ -163,6 +165,70 @@ __device__ __forceinline__ uint4 ld_v4(uint32_t addr) {
     return v;
 }
 
+// The non-finite values of keys [j0, j1), which the products left out, to a warp's rows (see odd_only): lane's row at `mine`, `parts` as
+// float32, sees `seen` keys.  For each element the first key of each kind; then row by row.
+template <typename TC, int D, bool PAGED>
+__device__ __noinline__ void add_odd(const AttnArgs* a, int b, int64_t k0, int hk, int j0, int j1, char* mine, bool parts, int seen) {
+    const int lane = threadIdx.x & 31;
+    RowTile t;
+    t.b = b, t.k0 = k0;
+    const KvRows<TC, PAGED> kv{*a, t, hk};
+    int up[4], down[4], nan[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) up[i] = down[i] = nan[i] = 0x7fffffff;
+#pragma unroll 4
+    for (int j = j1 - 1; j >= j0; --j) {
+        const float4 v4 = 4 * lane < D ? kv.get(true, j, 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (v[i] == INFINITY) up[i] = j;
+            if (v[i] == -INFINITY) down[i] = j;
+            if (v[i] != v[i]) nan[i] = j;
+        }
+    }
+    for (int r = 0; r < 32; ++r) {
+        const int sees = __shfl_sync(0xffffffffu, seen, r);
+        char* dst = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), r));
+        float add[4];
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            add[i] = (sees > up[i] ? INFINITY : 0.f) + (sees > down[i] ? -INFINITY : 0.f) + (sees > nan[i] ? NAN : 0.f);
+            any = any || add[i] != 0.f;
+        }
+        if (any) {
+            float* p32 = reinterpret_cast<float*>(dst) + 4 * lane;
+            __nv_bfloat16* p16 = reinterpret_cast<__nv_bfloat16*>(dst) + 4 * lane;
+            float4 x = parts ? load4f(p32) : load4f(p16);
+            x = make_float4(x.x + add[0], x.y + add[1], x.z + add[2], x.w + add[3]);
+            if (parts) store4(p32, x);
+            else store4(p16, x);
+        }
+        __syncwarp();
+    }
+}
+
+// What a widening thread has written of a value tile from row `from` on - chunks c and c + 1 of rows r0 + i ROWS - made finite;
+// *any says that something was not.
+template <int ROWS>
+__device__ __noinline__ void make_finite(uint32_t tile, int r0, int c, int from, int* any) {
+    bool odd = false;
+    for (int r = r0; r < BN; r += ROWS) {
+        if (r < from) continue;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t at = tile + tile_off(r, c + i);
+            uint4 v = ld_v4(at);
+            if (!any_odd<false>(v)) continue;
+            odd = true;
+            v = without_odd<false>(v);
+            st_v4(at, v.x, v.y, v.z, v.w);
+        }
+    }
+    if (odd) *reinterpret_cast<volatile int*>(any) = 1;
+}
+
 template <int D, int SRC>
 __global__ void __launch_bounds__(Cfg<D>::threads(SRC), Cfg<D>::PER_SM)
 attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -199,12 +265,16 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             jmax = max(jmax, je[w]);
         }
     }
+    // Keys that not all rows see: from `least` on.  From key tile jd on, tiles hold some (none: jd = jmax).
+    const int least = min(keys_seen(a, t, t.row0 / a.G), t.nk), jd = least < t.nk ? max(jb, least / BN) : jmax;
     const Wait wait{&sh.abort, a.err, a.timeout};
 
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(smem_u32(&sh.full[i]), NPROD);
             mbar_init(smem_u32(&sh.empty[i]), 1);
+            mbar_init(smem_u32(&sh.look[i]), 1);
+            mbar_init(smem_u32(&sh.clean[i]), 2);
         }
         mbar_init(smem_u32(&sh.q_full), 4 * NT);
         for (int w = 0; w < NT; ++w) {
@@ -214,7 +284,9 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             mbar_init(smem_u32(&sh.p_full[w]), 4);
             mbar_init(smem_u32(&sh.pv_done[w]), 1);
         }
-        sh.abort = 0;
+        sh.abort = sh.odd = 0;
+        sh.odd_hk = hk, sh.odd_b = t.b, sh.odd_k0 = t.k0;
+        sh.odd_from = max(least, jb * BN), sh.odd_to = min(jmax * BN, t.nk);
         fence_mbar_init();
     }
     if (warp == MMA_WARP) {
@@ -363,7 +435,6 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             const int64_t prow = ((int64_t)split * a.Tq + tok) * a.Hq + h;
             const bool parts = a.splits > 1;
             char* mine = parts ? reinterpret_cast<char*>(a.part_o + prow * D) : a.out.p + tok * a.out.st + h * a.out.sh;
-            bool finite = true;
             // The tile's queries are no longer read: their place takes the rows (as bf16, or half of each as
             // fp32), so that they leave with a row's chunks on neighbouring lanes.
             auto leave = [&](int bytes) {
@@ -386,10 +457,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     reg_fence(o);
                 }
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    o[i] = l == 0.f ? 0.f : o[i] * inv;
-                    finite = finite && fabsf(o[i]) < INFINITY;
-                }
+                for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;
                 if (parts) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
@@ -408,20 +476,10 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 if (parts) a.part_lse[prow] = lse2;
                 else if (a.lse) a.lse[tok * a.Hq + h] = lse2 * kLn2;
             }
-            // a row that masked keys of its tiles and is not finite: again over its own keys
-            uint32_t again = __ballot_sync(0xffffffffu, live && !finite && seen < min(je[w] * BN, t.nk));
-            while (again) {
-                const int src = __ffs(again) - 1;
-                again &= again - 1;
-                const int r = __shfl_sync(0xffffffffu, row, src), end = __shfl_sync(0xffffffffu, seen, src);
-                char* dst = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), src));
-                float4 o;
-                repair_row<typename std::conditional<SRC == kPagedE4m3, uint8_t, __nv_bfloat16>::type, D, SRC != kPacked>(
-                    a, t, hk, r, jb * BN, min(end, je[w] * BN), o);
-                if (4 * lane < D) {
-                    if (parts) store4(reinterpret_cast<float*>(dst) + 4 * lane, o);
-                    else store4(reinterpret_cast<__nv_bfloat16*>(dst) + 4 * lane, o);
-                }
+            if (__builtin_expect(*reinterpret_cast<volatile int*>(&sh.odd), 0)) {
+                __syncwarp();
+                add_odd<typename std::conditional<SRC == kPagedE4m3, uint8_t, __nv_bfloat16>::type, D, SRC != kPacked>(
+                    &a, sh.odd_b, sh.odd_k0, sh.odd_hk, sh.odd_from, sh.odd_to, mine, parts, live && l != 0.f ? seen : 0);
             }
         }
         tc_fence_before();
@@ -463,6 +521,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 if (je[w] > jb) issue_s(w, 0);
             mma_commit_w(smem_u32(&sh.empty[0]));
         }
+        uint32_t cleaned = 0;   // phases of `clean`
         for (int i = 0; ok && i < n; ++i) {
             const uint32_t iv = 2 * i + 1, ik = 2 * i + 2, sv = iv % NS, sk = ik % NS;
             const bool more = i + 1 < n;
@@ -482,6 +541,10 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     for (int p = 0; p < C::PANELS; ++p) st_v4(s_ring + sv * C::SLOT + p * (BN * 128) + x * 16, 0u, 0u, 0u, 0u);
                 fence_proxy_async();
                 __syncwarp();
+            }
+            if (SRC != kPagedE4m3 && jb + i >= jd) {   // not all rows see all of the tile's keys
+                if (!(ok = wait(&sh.clean[sv], (cleaned >> sv) & 1, 13))) break;
+                cleaned ^= 1u << sv;
             }
             if (!C::APART && more) {
                 if (!(ok = wait(&sh.full[sk], (ik / NS) & 1, 7))) break;
@@ -532,10 +595,38 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                             tma_load_4d(dst + p * (BN * 128) + lane * box * 128, tm, 64 * p, pos & (a.c.page_size - 1), hk, page, bar);
                     }
                 }
+                if ((issued & 1) && jb + (issued >> 1) >= jd) warp_arrive(&sh.look[slot]);
                 __syncwarp();
             }
             // no load may be in flight when the CTA's shared memory goes
             for (int i = max(0, issued - NS); i < issued; ++i) drain(&sh.full[i % NS], (i / NS) & 1, a.timeout);
+        } else {
+            // ---------------------------------------------------------- masked values made finite
+            uint32_t looked = 0;   // phases of `look`
+            for (int j = jd; j < jmax; ++j) {
+                const int iv = 2 * (j - jb) + 1, sv = iv % NS;
+                // The load warp says when the tile's load is under way: `full` then waits for that one's end.  The
+                // slot's next load comes after the tile's product, and that after `clean`.
+                if (!wait(&sh.look[sv], (looked >> sv) & 1, 14) || !wait(&sh.full[sv], (iv / NS) & 1, 15)) break;
+                looked ^= 1u << sv;
+                const int from = max(0, least - j * BN) * 8, to = min(BN, t.nk - j * BN) * 8;   // chunks of a panel; the swizzle stays in a row
+                bool odd = false;
+#pragma unroll 4
+                for (int x = from + lane + 32 * (warp - MMA_WARP - 2); x < to; x += 64)
+#pragma unroll
+                    for (int p = 0; p < C::PANELS; ++p) {
+                        const uint32_t at = s_ring + sv * C::SLOT + p * (BN * 128) + x * 16;
+                        uint4 v = ld_v4(at);
+                        if (any_odd<false>(v)) {
+                            odd = true;
+                            v = without_odd<false>(v);
+                            st_v4(at, v.x, v.y, v.z, v.w);
+                        }
+                    }
+                if (odd) *reinterpret_cast<volatile int*>(&sh.odd) = 1;
+                fence_proxy_async();
+                warp_arrive(&sh.clean[sv]);
+            }
         }
     } else {
         // ------------------------------------------------------------ 8-bit tiles widened to bf16
@@ -581,6 +672,18 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             if (it >= NS && !wait(&sh.empty[slot], ((it / NS) - 1) & 1, 9)) break;
             const uint32_t dst = s_ring + slot * C::SLOT;
             if (!(it & 1)) page = look_up(jb + (it >> 1) + 1);
+            else if (D == 128 && jb + (it >> 1) >= jd) {
+                // values that not all rows see: finite, as codes (D = 128: 312 us, in the slot 358) or in the slot (D = 64: 319, as codes 350)
+                bool odd = false;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if ((jb + (it >> 1)) * BN + r0 + u * ROWS < least) continue;
+                    odd = odd || any_odd<true>(code[u]);
+                    code[u] = without_odd<true>(code[u]);
+                    scale[u] = min(scale[u], 246u);
+                }
+                if (odd) *reinterpret_cast<volatile int*>(&sh.odd) = 1;
+            }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int r = r0 + u * ROWS;
@@ -598,7 +701,10 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     st_v4(dst + tile_off(r, 2 * c + 1), o[4], o[5], o[6], o[7]);
                 }
             }
-            if (it & 1) rows(jb + (it >> 1) + 1);
+            if (it & 1) {
+                rows(jb + (it >> 1) + 1);
+                if (D == 64 && jb + (it >> 1) >= jd) make_finite<ROWS>(dst, r0, 2 * c, max(0, least - (jb + (it >> 1)) * BN), &sh.odd);
+            }
             fence_proxy_async();
             warp_arrive(&sh.full[slot]);
 #pragma unroll

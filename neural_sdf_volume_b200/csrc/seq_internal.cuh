@@ -229,40 +229,24 @@ struct KvRows {
     }
 };
 
-// One row again over keys [j0, j1) alone, by a whole warp; lane's elements are 4 lane + 0..3 of
-// D = 128 and of D = 64 in its first 16 lanes.  Normalised values in o, result: log2 of the sum.
-// (keys that a row does not see have weight 0, and 0 * NaN or 0 * inf of their values would still
-// reach it through a matrix product: a row that ends up not finite while keys of its tiles were
-// masked is computed by this instead; never called with finite values)
-template <typename TC, int D, bool PAGED>
-__device__ __forceinline__ float repair_row(const AttnArgs& a, const RowTile& t, int hk, int row, int j0, int j1, float4& o) {
-    const int lane = threadIdx.x & 31;
-    const bool on = 4 * lane < D;
-    const KvRows<TC, PAGED> kv{a, t, hk};
-    float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
-    o = q;
-    if (on) q = load4f(reinterpret_cast<const __nv_bfloat16*>(a.q.p + (t.q0 + row / a.G) * a.q.st +
-                                                              (int64_t)(hk * a.G + row % a.G) * a.q.sh) + 4 * lane);
-    float m = -INFINITY, l = 0.f;
-    for (int j = j0; j < j1; ++j) {
-        float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
-        if (on) {
-            k = kv.get(false, j, 4 * lane);
-            v = kv.get(true, j, 4 * lane);
-        }
-        float s = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, q.w * k.w)));
-        for (int w = 16; w; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-        s *= a.scale_log2;
-        const float mn = fmaxf(m, s), base = mn == -INFINITY ? 0.f : mn;
-        const float f = exp2f(m - base), p = exp2f(s - base);
-        m = mn;
-        l = l * f + p;
-        o.x = fmaf(p, v.x, o.x * f), o.y = fmaf(p, v.y, o.y * f), o.z = fmaf(p, v.z, o.z * f), o.w = fmaf(p, v.w, o.w * f);
-    }
-    const float inv = l == 0.f ? 0.f : 1.0f / l;
-    o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
-    return l == 0.f ? -INFINITY : m + log2f(l);
+// Values of masked keys.  A key that a row does not see has weight 0, but 0 * NaN or 0 * inf of its value would still
+// reach the row through a matrix product.  Where rows of a block see different numbers of keys, the elements of the
+// values that not all of them see are therefore made finite (zeros for the others) before the product, and rows that do
+// see such an element get it added at the end, which leaves what its product with a positive weight would: infinity or NaN.
+// Whether 16 bytes of bf16 (E8: of e4m3 codes) hold a non-finite element: its exponent's (magnitude's) bits are all ones, and one more
+// reaches the sign's place.
+template <bool E8>
+__device__ __forceinline__ bool any_odd(uint4 v) {
+    constexpr uint32_t BITS = E8 ? 0x7f7f7f7fu : 0x7f807f80u, ONE = E8 ? 0x01010101u : 0x00800080u;
+    return ((((v.x & BITS) + ONE) | ((v.y & BITS) + ONE) | ((v.z & BITS) + ONE) | ((v.w & BITS) + ONE)) & (E8 ? 0x80808080u : 0x80008000u)) != 0u;
 }
+// these elements as zeros
+template <bool E8>
+__device__ __forceinline__ uint4 without_odd(uint4 v) {
+    auto f = [](uint32_t w) { return w & ~(E8 ? __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu) : __vcmpeq2(w & 0x7f807f80u, 0x7f807f80u)); };
+    return make_uint4(f(v.x), f(v.y), f(v.z), f(v.w));
+}
+__device__ __forceinline__ float odd_only(float x) { return fabsf(x) < INFINITY ? 0.f : x; }
 
 // rows of a tile of the few-rows kernel
 inline int rows_tile(int G, int64_t Tq, int B) { return Tq * G <= 8 * (B < Tq ? B : Tq) ? 8 : 16; }
