@@ -568,7 +568,8 @@ VDM_API vdm_status vdm_attention_paged(const vdm_attention* a, const vdm_heads* 
 
 /* The tensor-core attention kernels bound every wait on the device; one that gave
  * up sets an error word (one per device) and its outputs are not valid.  This
- * call waits for `stream`, then returns and clears it: OK or TIMEOUT (or CUDA).  */
+ * call waits for `stream`, then returns and clears the word of that stream's device
+ * (the default stream: the current device): OK or TIMEOUT (or CUDA).             */
 VDM_API vdm_status vdm_attention_status(vdm_stream stream);
 
 /* Test hook for failure detection (not needed for decoding).  mode n >= 1

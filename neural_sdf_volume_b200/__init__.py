@@ -662,9 +662,15 @@ def vdm_attention_paged(q, cache: KVCache, cu_q, kv_len, table, causal: bool = T
     return (_native or _load_seq()).attention_paged(q, cache, cu_q, kv_len, table, causal, scale, out, want_lse, workspace, stream)
 
 
-def vdm_attention_status(stream=None):
-    """Wait for the stream; raises if an attention call since the last check gave up a bounded wait."""
-    _check(_lib.vdm_attention_status(_stream(stream)))
+def vdm_attention_status(stream=None, device=None):
+    """Wait for the stream (by default the current one of ``device``, by default the current device); raises if an
+    attention call on that device gave up a bounded wait since the last check."""
+    torch = _torch()
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    if device is not None and torch.device(device).index not in (None, s.device.index):
+        raise ValueError(f"the stream is of {s.device}, not of {device}")
+    with torch.cuda.device(s.device):
+        _check(_lib.vdm_attention_status(s.cuda_stream))
 
 
 def vdm_surface_workspace_size(R: int) -> int:

@@ -333,6 +333,20 @@ vdm_status vdm_attention_paged(const vdm_attention* at, const vdm_heads* q, cons
 
 vdm_status vdm_attention_status(vdm_stream stream) {
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    // the word of the stream's device, whichever is current
+    struct On {
+        int was = 0, dev = 0;
+        bool moved = false;
+        ~On() {
+            if (moved) cudaSetDevice(was);
+        }
+    } on;
+    VDM_CUDA_TRY(cudaGetDevice(&on.was));
+    VDM_CUDA_TRY(cudaStreamGetDevice(s, &on.dev));
+    if (on.dev != on.was) {
+        VDM_CUDA_TRY(cudaSetDevice(on.dev));
+        on.moved = true;
+    }
     int* word = nullptr;
     VDM_TRY(attention_error_word(&word));
     int site = 0;

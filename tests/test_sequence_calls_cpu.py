@@ -1,0 +1,51 @@
+"""Token-sequence calls without a GPU: what their Python side hands to the library."""
+import ctypes as C
+import types
+
+import pytest
+import torch
+
+import neural_sdf_volume_b200 as vdm
+
+
+# ----------------------------------------------------------------- status of a device that is not the current one
+
+class FakeCuda:
+    """Two devices, 0 current, each with a default stream (handle 0) and one of its own."""
+
+    def __init__(self, monkeypatch, error):
+        self.current, self.asked = 0, []
+
+        class on:
+            def __init__(ctx, dev):
+                ctx.dev = torch.device(dev).index
+
+            def __enter__(ctx):
+                ctx.was, self.current = self.current, ctx.dev
+
+            def __exit__(ctx, *a):
+                self.current = ctx.was
+
+        def status(handle):                      # as the library: the default stream is the current device's
+            self.asked.append((self.current, handle))
+            return 5 if error == (handle - 1 if handle else self.current) else 0
+
+        monkeypatch.setattr(torch.cuda, "device", on)
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: self.stream(self.current if d is None else torch.device(d).index, 0))
+        monkeypatch.setattr(vdm, "_lib", types.SimpleNamespace(vdm_attention_status=status, vdm_last_error=lambda: b"expired",
+                                                              vdm_status_string=lambda s: b"timeout"))
+
+    def stream(self, dev, handle):
+        return types.SimpleNamespace(device=torch.device("cuda", dev), cuda_stream=handle)
+
+
+def test_status_is_of_the_streams_device(monkeypatch):
+    f = FakeCuda(monkeypatch, error=1)
+    vdm.vdm_attention_status()                                   # device 0: fine
+    for call in (lambda: vdm.vdm_attention_status(f.stream(1, 0)), lambda: vdm.vdm_attention_status(device="cuda:1"),
+                 lambda: vdm.vdm_attention_status(f.stream(1, 2))):
+        with pytest.raises(vdm.VdmError) as e:
+            call()
+        assert e.value.status == 5 and f.asked[-1][0] == 1 and f.current == 0
+    with pytest.raises(ValueError):
+        vdm.vdm_attention_status(f.stream(0, 0), device="cuda:1")
