@@ -540,7 +540,8 @@ typedef struct {
 
 /* Workspace of either attention call: Tq query tokens in B sequences, no sequence
  * with more than max_kv keys (packed: Tk; paged: max_pages * page_size).  Ask with a
- * call's own sizes: fewer tokens can need more (their keys are split further).   */
+ * call's own sizes and mask: fewer tokens, or causal ones, can need more (their keys
+ * are split further).                                                            */
 VDM_API vdm_status vdm_attention_workspace_size(const vdm_attention* a, int32_t B, int64_t Tq, int64_t max_kv,
                                                 size_t* bytes);
 

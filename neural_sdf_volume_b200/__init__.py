@@ -638,11 +638,15 @@ def vdm_cache_read(cache: KVCache, kv_len, table, cu, total: Optional[int] = Non
     return k, v
 
 
-def vdm_attention_workspace_size(Hq: int, Hk: int, D: int, dtype: str, B: int, Tq: int, max_kv: int) -> int:
-    n = C.c_size_t(0)
-    ca = CAttention(Hq, Hk, D, VDM_F32 if dtype == "f32" else VDM_BF16, 0, 1.0)
-    _check(_lib.vdm_attention_workspace_size(ca, B, Tq, max_kv, n))
-    return int(n.value)
+def vdm_attention_workspace_size(Hq: int, Hk: int, D: int, dtype: str, B: int, Tq: int, max_kv: int,
+                                 causal: Optional[bool] = None) -> int:
+    """Bytes that an attention call of these sizes needs (``max_kv``: the keys of a packed call, the table's reach of a
+    paged one); without ``causal``, of either kind."""
+    n, most = C.c_size_t(0), 0
+    for c in (0, 1) if causal is None else (int(causal),):
+        _check(_lib.vdm_attention_workspace_size(CAttention(Hq, Hk, D, VDM_F32 if dtype == "f32" else VDM_BF16, c, 1.0), B, Tq, max_kv, n))
+        most = max(most, n.value)
+    return int(most)
 
 
 def vdm_attention_packed(q, k, v, cu_q, cu_k=None, causal: bool = True, scale: Optional[float] = None, out=None,

@@ -49,3 +49,18 @@ def test_status_is_of_the_streams_device(monkeypatch):
         assert e.value.status == 5 and f.asked[-1][0] == 1 and f.current == 0
     with pytest.raises(ValueError):
         vdm.vdm_attention_status(f.stream(0, 0), device="cuda:1")
+
+
+# ----------------------------------------------------------------- workspace
+
+@pytest.mark.parametrize("Hq, Hk, D, dtype, B, T", [(4, 1, 128, "f32", 1, 3155), (2, 2, 128, "f32", 11, 6711), (8, 1, 64, "f32", 1, 10048),
+                                                    (8, 8, 64, "bf16", 6, 9000), (32, 8, 128, "bf16", 1, 1)])
+def test_workspace_is_enough_for_either_mask(Hq, Hk, D, dtype, B, T):
+    """A causal self-attention may split its keys further than one without a mask."""
+    need = []
+    for causal in (0, 1):
+        n = C.c_size_t(0)
+        vdm._check(vdm._lib.vdm_attention_workspace_size(vdm.CAttention(Hq, Hk, D, 0 if dtype == "f32" else 1, causal, 1.0), B, T, T, n))
+        need.append(n.value)
+        assert vdm.vdm_attention_workspace_size(Hq, Hk, D, dtype, B, T, T, causal=bool(causal)) == n.value
+    assert vdm.vdm_attention_workspace_size(Hq, Hk, D, dtype, B, T, T) == max(need)
