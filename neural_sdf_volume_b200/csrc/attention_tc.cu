@@ -232,7 +232,7 @@ __device__ __noinline__ void make_finite(uint32_t tile, int r0, int c, int from,
 template <int D, int SRC>
 __global__ void __launch_bounds__(Cfg<D>::threads(SRC), Cfg<D>::PER_SM)
 attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                    const __grid_constant__ AttnArgs a, const int tok_first) {
+                    const __grid_constant__ AttnArgs a, const bool tok_first_k, const bool tok_first_v) {
     using C = Cfg<D>;
     constexpr int NS = C::NS, NT = C::NT, MMA_WARP = 4 * NT;
     constexpr int NPROD = SRC == kPagedE4m3 ? C::WIDEN : 1;   // arrivals that complete a slot
@@ -574,6 +574,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     if (lane == 0) {
                         mbar_expect_tx(bar, C::SLOT);
                         const int tok = (int)(t.k0 + j0);
+                        const bool tok_first = issued & 1 ? tok_first_v : tok_first_k;
 #pragma unroll
                         for (int p = 0; p < C::PANELS; ++p)
                             tma_load_3d(dst + p * (BN * 128), tm, 64 * p, tok_first ? tok : hk, tok_first ? hk : tok, bar);
@@ -763,12 +764,12 @@ vdm_status paged_map(CUtensorMap* m, char* base, const CacheView& c) {
 }
 
 template <int D, int SRC>
-vdm_status launch(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, bool tok_first, cudaStream_t s) {
+vdm_status launch(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, bool tok_first_k, bool tok_first_v, cudaStream_t s) {
     auto kern = attention_tc_kernel<D, SRC>;
     static std::atomic<uint64_t> ready{0};
     VDM_TRY(prepare_kernel(ready, reinterpret_cast<const void*>(kern), smem_bytes<D>()));
     const int64_t tiles = row_tiles(a.Tq, a.G, a.B, tc_rows(D));
-    kern<<<tile_grid(a, tiles), Cfg<D>::threads(SRC), smem_bytes<D>(), s>>>(mk, mv, a, tok_first);
+    kern<<<tile_grid(a, tiles), Cfg<D>::threads(SRC), smem_bytes<D>(), s>>>(mk, mv, a, tok_first_k, tok_first_v);
     VDM_TRY(check_launch("attention_tc_kernel"));
     return a.splits > 1 ? launch_combine(a, VDM_BF16, s) : VDM_OK;
 }
@@ -782,17 +783,16 @@ vdm_status launch_attention_tc(const AttnArgs& a, cudaStream_t s) {
     memset(&mk, 0, sizeof(mk));
     memset(&mv, 0, sizeof(mv));
     if (a.paged && a.c.dtype == VDM_CACHE_E4M3)
-        return a.D == 64 ? launch<64, kPagedE4m3>(mk, mv, a, false, s) : launch<128, kPagedE4m3>(mk, mv, a, false, s);
+        return a.D == 64 ? launch<64, kPagedE4m3>(mk, mv, a, false, false, s) : launch<128, kPagedE4m3>(mk, mv, a, false, false, s);
     if (a.paged) {
         VDM_TRY(paged_map(&mk, a.c.k, a.c));
         VDM_TRY(paged_map(&mv, a.c.v, a.c));
-        return a.D == 64 ? launch<64, kPagedBf16>(mk, mv, a, false, s) : launch<128, kPagedBf16>(mk, mv, a, false, s);
+        return a.D == 64 ? launch<64, kPagedBf16>(mk, mv, a, false, false, s) : launch<128, kPagedBf16>(mk, mv, a, false, false, s);
     }
-    const bool tf = a.k.st < a.k.sh;
-    if (tf != (a.v.st < a.v.sh)) return launch_attention_simt(a, VDM_BF16, s);   // keys and values laid out differently
-    VDM_TRY(packed_map(&mk, a.k, a.Tk, a.Hk, a.D, tf));
-    VDM_TRY(packed_map(&mv, a.v, a.Tk, a.Hk, a.D, tf));
-    return a.D == 64 ? launch<64, kPacked>(mk, mv, a, tf, s) : launch<128, kPacked>(mk, mv, a, tf, s);
+    const bool tk = a.k.st < a.k.sh, tv = a.v.st < a.v.sh;   // each in its own order
+    VDM_TRY(packed_map(&mk, a.k, a.Tk, a.Hk, a.D, tk));
+    VDM_TRY(packed_map(&mv, a.v, a.Tk, a.Hk, a.D, tv));
+    return a.D == 64 ? launch<64, kPacked>(mk, mv, a, tk, tv, s) : launch<128, kPacked>(mk, mv, a, tk, tv, s);
 }
 
 }  // namespace vdm

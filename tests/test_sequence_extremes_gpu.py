@@ -101,3 +101,16 @@ def test_sums_when_scores_rise_and_fall_by_hundreds():
         q = torch.zeros(1, 4, 64, device="cuda", dtype=torch.bfloat16)
         q[0, :, 0] = torch.tensor([2.0 ** 10, 2.0 ** 11, -2.0 ** 11, 1.0])
         check_scaled(c, q, scale=1.0)
+
+
+# ----------------------------------------------------------------- layouts
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [20, 1500])
+def test_keys_and_values_in_different_orders(D, n):
+    """Head-major keys beside token-major values and the other way: the same kernel, the same bits."""
+    q, k, v = randn(1, n, 8, D), randn(2, n, 2, D), randn(3, n, 2, D)
+    hm = lambda x: x.transpose(0, 1).contiguous().transpose(0, 1)
+    want = vdm.vdm_attention_packed(q, k, v, offsets([n]))
+    assert torch.equal(vdm.vdm_attention_packed(q, hm(k), v, offsets([n])), want)
+    assert torch.equal(vdm.vdm_attention_packed(q, k, hm(v), offsets([n])), want)
