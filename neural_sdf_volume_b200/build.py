@@ -3,11 +3,13 @@ calls of the token-sequence operators, against torch's headers), in-tree.
 
 Usage: ``python -m neural_sdf_volume_b200.build`` or ``build()`` from Python.
 Objects go to ``_build/`` next to this file; the shared libraries are
-``libvdm.so`` and ``_seq.so`` in this package directory.
+``libvdm.so`` and ``_seq.so`` in this package directory.  Without torch (and a C++ compiler
+for its headers) the C library is built all the same; ``_seq.so`` is rebuilt when torch or Python change.
 """
 from __future__ import annotations
 
 import glob
+import importlib.metadata
 import os
 import subprocess
 import sys
@@ -29,6 +31,24 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", 
 def _deps_mtime() -> float:
     files = glob.glob(os.path.join(CSRC, "*")) + [os.path.join(ROOT, "include", "vdm.h"), __file__]
     return max(os.path.getmtime(f) for f in files)
+
+
+def _binding_versions() -> str | None:
+    """What _seq.so is built against, beside the sources; None without torch."""
+    try:
+        return f"torch {importlib.metadata.version('torch')}, python {sys.version}"
+    except importlib.metadata.PackageNotFoundError:
+        return None
+
+
+def _binding_fresh() -> bool:
+    versions, stamp = _binding_versions(), os.path.join(BUILD, "seq_binding.versions")
+    if versions is None:
+        return True
+    if not (os.path.exists(SEQ) and os.path.exists(stamp)) or os.path.getmtime(SEQ) < _deps_mtime():
+        return False
+    with open(stamp) as f:
+        return f.read() == versions
 
 
 def _compile_binding() -> str:
@@ -53,6 +73,8 @@ def _link_binding(obj: str) -> None:
         cmd += ["-L", p]
     _run([*cmd, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"], "linking _seq.so")
     os.replace(tmp, SEQ)
+    with open(os.path.join(BUILD, "seq_binding.versions"), "w") as f:
+        f.write(_binding_versions())
 
 
 def _run(cmd, what):
@@ -64,7 +86,7 @@ def _run(cmd, what):
 
 def build(force: bool = False, verbose: bool = False, extra: list | None = None) -> str:
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (LIB, SEQ)):
+    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime() and _binding_fresh():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     extra = extra or []
@@ -80,13 +102,15 @@ def build(force: bool = False, verbose: bool = False, extra: list | None = None)
         return obj
 
     with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
-        binding = ex.submit(_compile_binding)
+        binding = ex.submit(_compile_binding) if _binding_versions() else None
         objs = list(ex.map(compile_one, srcs))
-        binding = binding.result()
     tmp = LIB + ".tmp"
     _run([NVCC, *ARCH, "-shared", "-Xlinker", "-soname=libvdm.so", "-o", tmp, *objs], "linking libvdm.so")
     os.replace(tmp, LIB)
-    _link_binding(binding)
+    if binding is None:
+        sys.stderr.write("torch not found: _seq.so (the Python calls of the token-sequence operators) not built\n")
+    else:   # the C library stands whatever comes of this
+        _link_binding(binding.result())
     return LIB
 
 

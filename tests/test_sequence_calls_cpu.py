@@ -1,5 +1,7 @@
 """Token-sequence calls without a GPU: what their Python side hands to the library."""
 import ctypes as C
+import importlib.util
+import os
 import types
 
 import pytest
@@ -64,3 +66,53 @@ def test_workspace_is_enough_for_either_mask(Hq, Hk, D, dtype, B, T):
         need.append(n.value)
         assert vdm.vdm_attention_workspace_size(Hq, Hk, D, dtype, B, T, T, causal=bool(causal)) == n.value
     assert vdm.vdm_attention_workspace_size(Hq, Hk, D, dtype, B, T, T) == max(need)
+
+
+# ----------------------------------------------------------------- build
+
+@pytest.fixture
+def builder(monkeypatch, tmp_path):
+    """The build with its tools replaced by one that writes what it is asked for; `fail`: words of a command that fails."""
+    spec = importlib.util.spec_from_file_location("_build_under_test", os.path.join(os.path.dirname(vdm.__file__), "build.py"))
+    b = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(b)
+    for name, path in (("LIB", "libvdm.so"), ("SEQ", "_seq.so"), ("BUILD", "_build")):
+        monkeypatch.setattr(b, name, str(tmp_path / path))
+    b.ran, b.fail = [], None
+
+    def run(cmd, **kw):
+        b.ran.append(" ".join(cmd))
+        bad = b.fail is not None and b.fail in b.ran[-1]
+        if not bad:
+            with open(cmd[cmd.index("-o") + 1], "w"):
+                pass
+        return types.SimpleNamespace(returncode=int(bad), stdout="", stderr="")
+
+    monkeypatch.setattr(b.subprocess, "run", run)
+    return b
+
+
+def test_c_library_is_built_without_torch(builder, monkeypatch):
+    monkeypatch.setattr(builder, "_binding_versions", lambda: None)
+    assert builder.build() == builder.LIB and os.path.exists(builder.LIB) and not os.path.exists(builder.SEQ)
+    assert not any("seq_binding" in c for c in builder.ran)
+    n = len(builder.ran)
+    builder.build()
+    assert len(builder.ran) == n                                 # nothing left to do
+
+
+def test_c_library_stands_when_the_binding_fails(builder):
+    builder.fail = "seq_binding.cpp"
+    with pytest.raises(RuntimeError, match="seq_binding"):
+        builder.build()
+    assert os.path.exists(builder.LIB) and not os.path.exists(builder.SEQ)
+
+
+def test_binding_is_built_again_for_another_torch(builder, monkeypatch):
+    builder.build()
+    n = len(builder.ran)
+    builder.build()
+    assert os.path.exists(builder.SEQ) and len(builder.ran) == n
+    monkeypatch.setattr(builder, "_binding_versions", lambda: "torch 99, python 4")
+    builder.build()
+    assert any("seq_binding" in c for c in builder.ran[n:])
