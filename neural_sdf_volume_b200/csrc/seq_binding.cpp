@@ -7,6 +7,7 @@
 
 #include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/AutogradState.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -55,6 +56,8 @@ const at::Tensor& tensor(const char* name, PyObject* o) {
 void no_grad(const char* name, const at::Tensor& t) {
     if (t.requires_grad() && at::GradMode::is_enabled())
         refuse("%s requires a gradient, which this call does not compute: detach it, or call under torch.no_grad()", name);
+    if (c10::AutogradState::get_tls_state().get_fw_grad_mode() && t._fw_grad(0).defined())
+        refuse("%s carries a forward-mode tangent, which this call does not propagate: unpack it first", name);
 }
 
 const at::Tensor& cuda_tensor(const char* name, PyObject* o) {
@@ -166,6 +169,7 @@ void read_cache(PyObject* o, Cache& out) {
         Ref r(PyObject_GetAttrString(o, n));
         if (r.p == Py_None) return false;
         hold = tensor(n, r.p);
+        no_grad(n, hold);
         return true;
     };
     at::Tensor &k = out.hold[0], &v = out.hold[1];
@@ -251,6 +255,7 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         f = tensor("rope.inv_freq", fr.p);
         if (f.scalar_type() != at::kDouble || f.dim() != 1 || f.device() != dev || !f.is_contiguous() || f.size(0) > INT_MAX / 2)
             refuse("rope.inv_freq must be a contiguous float64 tensor [rot_dim/2] on %s", dev.str().c_str());
+        no_grad("rope.inv_freq", f);
         if (a[2] == Py_None) refuse("a rotation needs positions");
         rope.rot_dim = (int32_t)(2 * f.size(0));
         rope.interleaved = truth(in.p);

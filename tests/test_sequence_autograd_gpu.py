@@ -1,0 +1,57 @@
+"""Token-sequence calls beside autograd and threads: what would have to be differentiated is refused, whichever tensor asks for it."""
+import pytest
+import torch
+import torch.autograd.forward_ad as fw
+
+import neural_sdf_volume_b200 as vdm
+from test_sequence_gpu import Cached, ints, offsets, randn
+
+pytestmark = pytest.mark.gpu
+
+
+def calls():
+    """Name of a tensor -> a call of it, all others plain."""
+    q, k, v = (randn(s, 5, 4, 64) for s in (1, 2, 3))
+    pos, cu, g = torch.arange(5, dtype=torch.int32, device="cuda"), offsets([5]), torch.ones(64, device="cuda")
+    c = Cached("bf16", 4, 64, 16, [5])
+    rope = lambda f: vdm.Rope(f)
+    f = vdm.Rope.make(64).inv_freq
+    paged = lambda x=q, ck=c.cache.k, cv=c.cache.v: vdm.vdm_attention_paged(x, vdm.KVCache(ck, cv), cu, c.kv_len, c.table)
+    return {
+        "inv_freq": (f, lambda x: vdm.vdm_qk_norm_rope(q, None, pos, rope(x))),
+        "norm q": (q, lambda x: vdm.vdm_qk_norm_rope(x, None, pos, rope(f))),
+        "norm k": (k, lambda x: vdm.vdm_qk_norm_rope(q, x, pos, rope(f))),
+        "gain": (g, lambda x: vdm.vdm_qk_norm_rope(q, k, pos, rope(f), q_gain=x)),
+        "packed q": (q, lambda x: vdm.vdm_attention_packed(x, k, v, cu)),
+        "packed v": (v, lambda x: vdm.vdm_attention_packed(q, k, x, cu)),
+        "paged q": (q, lambda x: paged(x)),
+        "cache k": (c.cache.k, lambda x: paged(ck=x)),
+        "cache v": (c.cache.v, lambda x: paged(cv=x)),
+        "read": (c.cache.k, lambda x: vdm.vdm_cache_read(vdm.KVCache(x, c.cache.v), c.kv_len, c.table, cu, total=5)),
+        "write": (k, lambda x: vdm.vdm_cache_write(c.cache, x, v, cu, c.kv_len, c.table)),
+        "written": (c.cache.v, lambda x: vdm.vdm_cache_write(vdm.KVCache(c.cache.k, x), k, v, cu, c.kv_len, c.table)),
+    }
+
+
+NAMES = ["inv_freq", "norm q", "norm k", "gain", "packed q", "packed v", "paged q", "cache k", "cache v", "read", "write", "written"]
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_gradients_are_refused(name):
+    x, call = calls()[name]
+    call(x)
+    y = x.clone().requires_grad_()
+    with pytest.raises(ValueError, match="gradient"):
+        call(y)
+    with torch.no_grad():
+        call(y)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_tangents_are_refused(name):
+    x, call = calls()[name]
+    with fw.dual_level():
+        y = fw.make_dual(x.clone(), torch.ones_like(x))
+        with pytest.raises(ValueError, match="tangent"):
+            call(y)
+        call(fw.unpack_dual(y).primal)

@@ -116,3 +116,21 @@ def test_binding_is_built_again_for_another_torch(builder, monkeypatch):
     monkeypatch.setattr(builder, "_binding_versions", lambda: "torch 99, python 4")
     builder.build()
     assert any("seq_binding" in c for c in builder.ran[n:])
+
+
+# ----------------------------------------------------------------- gradients
+
+def test_cache_that_requires_gradients_is_refused():
+    c = vdm.KVCache.create(2, 16, 8, 64, device="cpu")
+    i = torch.zeros(2, dtype=torch.int32)
+    out = (torch.zeros(1, 8, 64, dtype=torch.bfloat16),) * 2
+    c.v.requires_grad_()
+    with pytest.raises(ValueError, match="gradient"):
+        vdm.vdm_cache_read(c, i[:1], i[None], i, out=out)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):          # as far as a host tensor gets
+        vdm.vdm_cache_read(c, i[:1], i[None], i, out=out)
+    c.v = c.v.detach()
+    with torch.autograd.forward_ad.dual_level():
+        c.k = torch.autograd.forward_ad.make_dual(c.k, torch.ones_like(c.k))
+        with pytest.raises(ValueError, match="tangent"):
+            vdm.vdm_cache_read(c, i[:1], i[None], i, out=out)
