@@ -60,6 +60,11 @@ void no_grad(const char* name, const at::Tensor& t) {
         refuse("%s carries a forward-mode tangent, which this call does not propagate: unpack it first", name);
 }
 
+// written in place: a graph that has kept the tensor notices (inference tensors have no version)
+void written(const at::Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 const at::Tensor& cuda_tensor(const char* name, PyObject* o) {
     const at::Tensor& t = tensor(name, o);
     if (!t.is_cuda()) refuse("%s must be a CUDA tensor (got one on %s)", name, t.device().str().c_str());
@@ -273,6 +278,8 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     check(vdm_qk_norm_rope(dt, T, (int32_t)Hq, (int32_t)Hk, (int32_t)D, &hq, with_k ? &hk : nullptr, gq, gk, eps,
                            a[3] == Py_None ? nullptr : &rope, pos, &hqo, with_k ? &hko : nullptr, on.stream));
+    if (a[7] != Py_None) written(qo);
+    if (with_k && a[8] != Py_None) written(ko);
     Ref r0(a[7] == Py_None ? THPVariable_Wrap(qo) : Py_NewRef(a[7]));
     Ref r1(!with_k ? Py_NewRef(Py_None) : a[8] == Py_None ? THPVariable_Wrap(ko) : Py_NewRef(a[8]));
     return PyTuple_Pack(2, r0.p, r1.p);
@@ -292,6 +299,8 @@ PyObject* cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const vdm_heads hk = heads("k", k, k, T, c.c.H, c.c.D), hv = heads("v", v, k, T, c.c.H, c.c.D);
     On on(k.device(), a[6]);
     check(vdm_cache_write(&c.c, dt, &hk, &hv, T, t.cu, t.len, t.table, t.max_pages, t.B, on.stream));
+    for (const at::Tensor& x : c.hold)
+        if (x.defined()) written(x);
     Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
 }
@@ -311,6 +320,7 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (k.device() != c.k->device()) refuse("out is on %s, the cache on %s", k.device().str().c_str(), c.k->device().str().c_str());
     On on(k.device(), a[6]);
     check(vdm_cache_read(&c.c, dt, t.len, t.table, t.max_pages, t.cu, t.B, T, &hk, &hv, on.stream));
+    written(k), written(v);
     Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
 }
@@ -348,6 +358,7 @@ struct Attention {
     float* lse_ptr() const { return lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr; }
     void* ws_ptr() const { return ws.defined() ? ws.data_ptr() : nullptr; }
     PyObject* result() const {
+        if (given != Py_None) written(out);
         Ref o(given == Py_None ? THPVariable_Wrap(out) : Py_NewRef(given));
         if (!lse.defined()) return Py_NewRef(o.p);
         Ref l(THPVariable_Wrap(lse));

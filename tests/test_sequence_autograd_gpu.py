@@ -55,3 +55,29 @@ def test_tangents_are_refused(name):
         with pytest.raises(ValueError, match="tangent"):
             call(y)
         call(fw.unpack_dual(y).primal)
+
+
+@pytest.mark.parametrize("name", ["norm", "packed", "paged", "write", "read"])
+def test_tensors_written_in_place_tell_a_graph_that_kept_them(name):
+    """A product that has kept a factor for its backward pass finds it changed, as after torch's own in-place operations."""
+    q, k = randn(1, 5, 4, 64), randn(2, 5, 4, 64)
+    c = Cached("bf16", 4, 64, 16, [5])
+    cu, x = offsets([5]), torch.zeros(5, 4, 64, device="cuda", dtype=torch.bfloat16)
+    target, call = {
+        "norm": (x, lambda: vdm.vdm_qk_norm_rope(q, k, q_gain=torch.ones(64, device="cuda"), k_out=x)),
+        "packed": (x, lambda: vdm.vdm_attention_packed(q, k, k, cu, out=x)),
+        "paged": (x, lambda: vdm.vdm_attention_paged(q, c.cache, cu, c.kv_len, c.table, out=x)),
+        "write": (c.cache.v, lambda: vdm.vdm_cache_write(c.cache, q, k, cu, c.kv_len, c.table)),
+        "read": (x, lambda: vdm.vdm_cache_read(c.cache, c.kv_len, c.table, cu, out=(torch.empty_like(x), x))),
+    }[name]
+    w = torch.ones((), device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    y = (target * w).sum()
+    before = target._version
+    call()
+    assert target._version > before
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.backward()
+    with torch.inference_mode():                     # no versions there
+        z = torch.empty_like(x)
+        vdm.vdm_attention_packed(q, k, k, cu, out=z)
+    vdm.vdm_attention_packed(q, k, k, cu, out=z)
