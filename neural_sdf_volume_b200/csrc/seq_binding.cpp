@@ -157,6 +157,19 @@ struct On {
     }
 };
 
+// Without the interpreter's lock, as the ctypes calls: a launch waits while the device's queue is full, an allocation for the
+// device.  f touches no Python object.
+template <typename F> auto unlocked(F f) {
+    struct Gate {
+        PyThreadState* s = PyEval_SaveThread();
+        ~Gate() { PyEval_RestoreThread(s); }
+    } gate;
+    return f();
+}
+at::Tensor empty(c10::IntArrayRef sizes, const at::TensorOptions& o) {
+    return unlocked([&] { return at::empty(sizes, o); });
+}
+
 void check(vdm_status s) {
     if (s == VDM_OK) return;
     Ref r(PyObject_CallFunction(g_check, "i", (int)s));
@@ -270,14 +283,14 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     const float eps = (float)number(a[6]);
     On on(dev, a[9]);
-    at::Tensor qo = a[7] == Py_None ? at::empty({T, Hq, D}, q.options()) : tensor("q_out", a[7]), ko;
+    at::Tensor qo = a[7] == Py_None ? empty({T, Hq, D}, q.options()) : tensor("q_out", a[7]), ko;
     const vdm_heads hqo = heads("q_out", qo, q, T, Hq, D);
     if (with_k) {
-        ko = a[8] == Py_None ? at::empty({T, Hk, D}, q.options()) : tensor("k_out", a[8]);
+        ko = a[8] == Py_None ? empty({T, Hk, D}, q.options()) : tensor("k_out", a[8]);
         hko = heads("k_out", ko, q, T, Hk, D);
     }
-    check(vdm_qk_norm_rope(dt, T, (int32_t)Hq, (int32_t)Hk, (int32_t)D, &hq, with_k ? &hk : nullptr, gq, gk, eps,
-                           a[3] == Py_None ? nullptr : &rope, pos, &hqo, with_k ? &hko : nullptr, on.stream));
+    check(unlocked([&] { return vdm_qk_norm_rope(dt, T, (int32_t)Hq, (int32_t)Hk, (int32_t)D, &hq, with_k ? &hk : nullptr, gq, gk, eps,
+                           a[3] == Py_None ? nullptr : &rope, pos, &hqo, with_k ? &hko : nullptr, on.stream); }));
     if (a[7] != Py_None) written(qo);
     if (with_k && a[8] != Py_None) written(ko);
     Ref r0(a[7] == Py_None ? THPVariable_Wrap(qo) : Py_NewRef(a[7]));
@@ -298,7 +311,7 @@ PyObject* cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tables t = read_tables(c, a[3], a[4], a[5], k.device());
     const vdm_heads hk = heads("k", k, k, T, c.c.H, c.c.D), hv = heads("v", v, k, T, c.c.H, c.c.D);
     On on(k.device(), a[6]);
-    check(vdm_cache_write(&c.c, dt, &hk, &hv, T, t.cu, t.len, t.table, t.max_pages, t.B, on.stream));
+    check(unlocked([&] { return vdm_cache_write(&c.c, dt, &hk, &hv, T, t.cu, t.len, t.table, t.max_pages, t.B, on.stream); }));
     for (const at::Tensor& x : c.hold)
         if (x.defined()) written(x);
     Py_RETURN_NONE;
@@ -319,7 +332,7 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const vdm_heads hk = heads("k", k, k, T, c.c.H, c.c.D), hv = heads("v", v, k, T, c.c.H, c.c.D);
     if (k.device() != c.k->device()) refuse("out is on %s, the cache on %s", k.device().str().c_str(), c.k->device().str().c_str());
     On on(k.device(), a[6]);
-    check(vdm_cache_read(&c.c, dt, t.len, t.table, t.max_pages, t.cu, t.B, T, &hk, &hv, on.stream));
+    check(unlocked([&] { return vdm_cache_read(&c.c, dt, t.len, t.table, t.max_pages, t.cu, t.B, T, &hk, &hv, on.stream); }));
     written(k), written(v);
     Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
@@ -342,12 +355,12 @@ struct Attention {
     }
     void allocate(const at::Tensor& q, int32_t B, int64_t max_kv, PyObject* const* a) {
         const int64_t T = q.size(0);
-        out = given == Py_None ? at::empty({T, q.size(1), q.size(2)}, q.options()) : tensor("out", given);
+        out = given == Py_None ? empty({T, q.size(1), q.size(2)}, q.options()) : tensor("out", given);
         ho = heads("out", out, q, T, q.size(1), q.size(2));
-        if (truth(a[3])) lse = at::empty({T, q.size(1)}, q.options().dtype(at::kFloat));
+        if (truth(a[3])) lse = empty({T, q.size(1)}, q.options().dtype(at::kFloat));
         if (a[4] == Py_None) {
             check(vdm_attention_workspace_size(&p, B, T, max_kv, &ws_bytes));
-            if (ws_bytes) ws = at::empty({(int64_t)ws_bytes}, q.options().dtype(at::kByte));
+            if (ws_bytes) ws = empty({(int64_t)ws_bytes}, q.options().dtype(at::kByte));
         } else {
             ws = tensor("workspace", a[4]);
             if (ws.device() != q.device() || !ws.is_contiguous())
@@ -385,7 +398,7 @@ PyObject* attention_packed(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t* pk = a[4] == Py_None ? pq : index("cu_k", tensor("cu_k", a[4]), q.device(), {B + 1});
     On on(q.device(), a[10]);
     at.allocate(q, B, Tk, a + 5);
-    check(vdm_attention_packed(&at.p, &hq, &hk, &hv, pq, pk, B, q.size(0), Tk, &at.ho, at.lse_ptr(), at.ws_ptr(), at.ws_bytes, on.stream));
+    check(unlocked([&] { return vdm_attention_packed(&at.p, &hq, &hk, &hv, pq, pk, B, q.size(0), Tk, &at.ho, at.lse_ptr(), at.ws_ptr(), at.ws_bytes, on.stream); }));
     return at.result();
     END_HANDLE_TH_ERRORS
 }
@@ -403,8 +416,8 @@ PyObject* attention_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tables t = read_tables(c, a[2], a[3], a[4], q.device());
     On on(q.device(), a[10]);
     at.allocate(q, t.B, (int64_t)t.max_pages * c.c.page_size, a + 5);
-    check(vdm_attention_paged(&at.p, &hq, &c.c, t.cu, t.len, t.table, t.max_pages, t.B, q.size(0), &at.ho, at.lse_ptr(), at.ws_ptr(),
-                              at.ws_bytes, on.stream));
+    check(unlocked([&] { return vdm_attention_paged(&at.p, &hq, &c.c, t.cu, t.len, t.table, t.max_pages, t.B, q.size(0), &at.ho, at.lse_ptr(), at.ws_ptr(),
+                              at.ws_bytes, on.stream); }));
     return at.result();
     END_HANDLE_TH_ERRORS
 }

@@ -81,3 +81,37 @@ def test_tensors_written_in_place_tell_a_graph_that_kept_them(name):
         z = torch.empty_like(x)
         vdm.vdm_attention_packed(q, k, k, cu, out=z)
     vdm.vdm_attention_packed(q, k, k, cu, out=z)
+
+
+def test_other_threads_run_while_a_launch_waits():
+    """More calls than a stream's queue holds, behind a second of other work: a thread that only counts goes on meanwhile."""
+    import threading
+    import time
+    q, cu = randn(1, 5, 4, 64), offsets([5])
+    f = lambda: vdm.vdm_attention_packed(q, q, q, cu, out=out)
+    out = torch.empty_like(q)
+    f()
+    torch.cuda.synchronize()
+    gap, stop = [0.0], threading.Event()
+
+    def count():
+        last = time.perf_counter()
+        while not stop.is_set():
+            time.sleep(0.001)
+            now = time.perf_counter()
+            gap[0], last = max(gap[0], now - last), now
+
+    t = threading.Thread(target=count)
+    t.start()
+    try:
+        torch.cuda._sleep(2_000_000_000)             # cycles: a second
+        start = time.perf_counter()
+        for _ in range(4000):
+            f()
+        waited = time.perf_counter() - start
+    finally:
+        stop.set()
+        t.join()
+    torch.cuda.synchronize()
+    assert waited > 0.6, f"the queue held all of them ({waited:.3f} s)"
+    assert gap[0] < 0.4, f"held up for {gap[0]:.3f} s"
