@@ -449,8 +449,11 @@ VDM_API vdm_status vdm_surface_case_table(uint8_t* ntri, uint8_t* tri);
  *     strides), and rows do not overlap.  D is 64 or 128; dtype f32 or bf16.
  *   - Sequence b owns the tokens [cu[b], cu[b+1]) of a packed tensor (cu: B+1
  *     int32, device).  Tokens outside every sequence (behind cu[B]) have no
- *     influence and are not written.  Offsets are clamped to [0, T]; a decreasing pair is an
- *     empty sequence.  Nothing else about them is checked.
+ *     influence and are not written.  Offsets are clamped to [0, T] and must not
+ *     decrease (equal neighbours: an empty sequence; unused entries of a batch of
+ *     fixed size repeat the last offset).  They are not checked: with decreasing ones
+ *     it is not specified which rows are written and from which keys, but nothing
+ *     outside the tensors is read or written.
  *   - Sums, norms and softmax statistics are float32.                       */
 typedef struct {
     void* data;              /* element [0][0][0]                                */

@@ -509,7 +509,8 @@ def vdm_refine_level(f, fine=None, parents=None, workspace=None, stream=None):
 # ----------------------------------------------------------------- token-sequence operators
 # Packed tensors are [tokens, heads, D] with any 16-byte aligned token and head strides
 # (slices of a fused projection, or ``K[b].transpose(0, 1)`` of ``vdm_precompute_kv``'s
-# result).  Sequence b owns tokens cu[b] .. cu[b+1] - 1.  The calls return without waiting, and have no
+# result).  Sequence b owns tokens cu[b] .. cu[b+1] - 1; offsets must not decrease (unused entries of a batch of fixed
+# size repeat the last one).  The calls return without waiting, and have no
 # backward pass: a tensor that requires a gradient is refused outside torch.no_grad().
 PAGE_SIZES = (16, 32, 64, 128, 256)
 

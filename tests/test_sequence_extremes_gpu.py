@@ -114,3 +114,50 @@ def test_keys_and_values_in_different_orders(D, n):
     want = vdm.vdm_attention_packed(q, k, v, offsets([n]))
     assert torch.equal(vdm.vdm_attention_packed(q, hm(k), v, offsets([n])), want)
     assert torch.equal(vdm.vdm_attention_packed(q, k, hm(v), offsets([n])), want)
+
+
+# ----------------------------------------------------------------- offsets
+
+def inside(shape, dtype):
+    """A tensor in the middle of a larger one, and whether what surrounds it is as it was."""
+    n = int(np.prod(shape))
+    whole = torch.full((n + 2 * 65536,), 7.0, device="cuda", dtype=dtype)
+    return whole[65536:65536 + n].view(shape), lambda: bool((whole[:65536] == 7.0).all() and (whole[65536 + n:] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("cu", [[0, 40, 20], [10, 5, 20], [40, 60, 0, 40], [0, 30, 60, 0, 0], [-9, 500, 3, -1, 70, 64], [900, 0, 900, 0, 900]])
+@pytest.mark.parametrize("keys", [64, 3000, 40000])                  # one part of the keys, or several
+def test_offsets_that_decrease_touch_nothing_outside(dtype, cu, keys):
+    """What they mean is not specified; memory around the tensors stays as it was, and what is written is an average of values."""
+    T, B = 64, len(cu) - 1
+    q = randn(1, T, 8, 64, dtype=dtype)
+    out, untouched = inside((T, 8, 64), S.DT[dtype])
+    k, v = randn(2, keys, 2, 64, dtype=dtype), randn(3, keys, 2, 64, dtype=dtype)
+    top = float(v.abs().max())
+    vdm.vdm_attention_packed(q, k, v, ints(cu), ints([x * keys // 64 for x in cu]), causal=False, out=out)
+    vdm.vdm_attention_packed(q, k, v, ints(cu), ints([0, keys] * B)[:B + 1].contiguous(), causal=True, out=out)
+    vdm.vdm_attention_status()
+    assert untouched() and (((out.abs() <= top * 1.01) | (out == 7.0)).all())
+    c = S.Cached("e4m3", 2, 64, 16, [min(keys, 3000)] * B, seed=2)
+    vdm.vdm_attention_paged(q, c.cache, ints(cu), c.kv_len, c.table, out=out)
+    vdm.vdm_attention_status()
+    (rk, ku), (rv, vu) = inside((T, 2, 64), S.DT[dtype]), inside((T, 2, 64), S.DT[dtype])
+    vdm.vdm_cache_read(c.cache, c.kv_len, c.table, ints(cu), out=(rk, rv))
+    vdm.vdm_cache_write(c.cache, rk, rv, ints(cu), c.kv_len, c.table)
+    torch.cuda.synchronize()
+    assert untouched() and ku() and vu()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens, keys", [([40, 50], 60), ([3, 1], 30000), ([1], 40000)])
+def test_batches_of_fixed_size_repeat_the_last_offset(dtype, lens, keys):
+    """Unused entries change nothing, whatever the route."""
+    q, kv = randn(1, sum(lens) + 3, 8, 64, dtype=dtype), randn(2, keys * len(lens), 4, 64, dtype=dtype)
+    cu, ck = [0, *np.cumsum(lens).tolist()], [keys * i for i in range(len(lens) + 1)]
+    k, v, n = kv[:, :2], kv[:, 2:], sum(lens)
+    want = vdm.vdm_attention_packed(q, k, v, ints(cu), ints(ck), causal=False)
+    for extra in (1, 40):
+        got = vdm.vdm_attention_packed(q, k, v, ints(cu + cu[-1:] * extra), ints(ck + ck[-1:] * extra), causal=False)
+        tol, _ = S.tolerance(np64(q), np64(k), np64(v), np64(want), 0.125, dtype)
+        close(got[:n], np64(want)[:n], 2 * tol[:n])
