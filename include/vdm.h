@@ -571,7 +571,9 @@ VDM_API vdm_status vdm_attention_paged(const vdm_attention* a, const vdm_heads* 
                                        vdm_stream stream);
 
 /* The tensor-core attention kernels bound every wait on the device; one that gave
- * up sets an error word (one per device) and its outputs are not valid.  This
+ * up sets an error word (one per device) and leaves NaN in the rows of out and lse
+ * that it could not finish.  The word does not say which call it was: whoever asks
+ * first is told, and later ones are not, so that one place a device should ask.  This
  * call waits for `stream`, then returns and clears the word of that stream's device
  * (the default stream: the current device): OK or TIMEOUT (or CUDA).             */
 VDM_API vdm_status vdm_attention_status(vdm_stream stream);

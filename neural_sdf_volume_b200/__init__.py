@@ -510,7 +510,8 @@ def vdm_refine_level(f, fine=None, parents=None, workspace=None, stream=None):
 # Packed tensors are [tokens, heads, D] with any 16-byte aligned token and head strides
 # (slices of a fused projection, or ``K[b].transpose(0, 1)`` of ``vdm_precompute_kv``'s
 # result).  Sequence b owns tokens cu[b] .. cu[b+1] - 1; offsets must not decrease (unused entries of a batch of fixed
-# size repeat the last one).  The calls return without waiting, and have no
+# size repeat the last one).  An attention whose bounded waits on the device expire leaves NaN rows, which
+# vdm_attention_status reports once.  The calls return without waiting, and have no
 # backward pass: a tensor that requires a gradient is refused outside torch.no_grad().
 PAGE_SIZES = (16, 32, 64, 128, 256)
 
@@ -669,7 +670,8 @@ def vdm_attention_paged(q, cache: KVCache, cu_q, kv_len, table, causal: bool = T
 
 def vdm_attention_status(stream=None, device=None):
     """Wait for the stream (by default the current one of ``device``, by default the current device); raises if an
-    attention call on that device gave up a bounded wait since the last check."""
+    attention call on that device, on whichever stream, gave up a bounded wait since the last check.  The rows that such a
+    call could not finish are NaN."""
     torch = _torch()
     s = stream if stream is not None else torch.cuda.current_stream(device)
     if device is not None and torch.device(device).index not in (None, s.device.index):

@@ -40,7 +40,8 @@
 // not all rows of the CTA see lose their non-finite elements there, by the two warps that are idle otherwise (8-bit: while they
 // are widened), and the rows that do see such an element get it at the end: see odd_only.
 //
-// Every wait is bounded; on expiry the kernel sets the error word, winds down and frees TMEM.
+// Every wait is bounded; on expiry the kernel sets the error word, leaves NaN in the rows it could not finish, winds down and
+// frees TMEM.
 #include <cuda.h>
 #include <string.h>
 
@@ -207,6 +208,16 @@ __device__ __noinline__ void add_odd(const AttnArgs* a, int b, int64_t k0, int h
         }
         __syncwarp();
     }
+}
+
+// A row that could not be finished: NaN, so that it is not taken for a result.
+__device__ __noinline__ void give_up(const AttnArgs* a, int split, int64_t tok, int h) {
+    const int64_t prow = ((int64_t)split * a->Tq + tok) * a->Hq + h;
+    const bool parts = a->splits > 1;
+    char* const row = parts ? reinterpret_cast<char*>(a->part_o + prow * a->D) : a->out.p + tok * a->out.st + h * a->out.sh;
+    for (int i = 0; i < a->D * (parts ? 4 : 2); i += 16) *reinterpret_cast<uint4*>(row + i) = make_uint4(~0u, ~0u, ~0u, ~0u);
+    if (parts) a->part_lse[prow] = NAN;
+    else if (a->lse) a->lse[tok * a->Hq + h] = NAN;
 }
 
 // What a widening thread has written of a value tile from row `from` on - chunks c and c + 1 of rows r0 + i ROWS - made finite;
@@ -482,6 +493,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     &a, sh.odd_b, sh.odd_k0, sh.odd_hk, sh.odd_from, sh.odd_to, mine, parts, live && l != 0.f ? seen : 0);
             }
         }
+        if (!ok && live) give_up(&a, split, tok, h);
         tc_fence_before();
     } else {
       regs_down<C::regs_other(SRC)>();

@@ -161,3 +161,33 @@ def test_batches_of_fixed_size_repeat_the_last_offset(dtype, lens, keys):
         got = vdm.vdm_attention_packed(q, k, v, ints(cu + cu[-1:] * extra), ints(ck + ck[-1:] * extra), causal=False)
         tol, _ = S.tolerance(np64(q), np64(k), np64(v), np64(want), 0.125, dtype)
         close(got[:n], np64(want)[:n], 2 * tol[:n])
+
+
+# ----------------------------------------------------------------- calls that give up
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kind, new, total", [("packed", 2000, 2000), ("bf16", 520, 5000), ("e4m3", 520, 5000)])
+def test_a_call_that_gives_up_leaves_nan(D, kind, new, total):
+    """A withheld signal: every row of out and lse says that it is no result, also where parts of the keys are joined."""
+    q = randn(1, new + 3, 8, D)
+    out = torch.full((new + 3, 8, D), 7.0, device="cuda", dtype=torch.bfloat16)
+    if kind == "packed":
+        k, v = randn(2, total, 2, D), randn(3, total, 2, D)
+        call = lambda: vdm.vdm_attention_packed(q, k, v, offsets([new]), offsets([total]), want_lse=True, out=out)
+    else:
+        c = S.Cached(kind, 2, D, 32, [total], seed=1)
+        call = lambda: vdm.vdm_attention_paged(q, c.cache, offsets([new]), c.kv_len, c.table, want_lse=True, out=out)
+    want, wl = (x.clone() for x in call())
+    vdm.vdm_attention_status()
+    vdm.vdm_debug_inject(1, 20_000_000)            # cycles of a wait, about 10 ms
+    try:
+        got, lse = call()
+        with pytest.raises(vdm.VdmError) as e:
+            vdm.vdm_attention_status()
+        assert e.value.status == 5
+        assert torch.isnan(got[:new]).all() and torch.isnan(lse[:new]).all() and (got[new:] == 7.0).all()
+    finally:
+        vdm.vdm_debug_inject(0, 0)
+    got, lse = call()
+    vdm.vdm_attention_status()
+    assert torch.equal(got, want) and torch.equal(lse[:new], wl[:new])
