@@ -134,3 +134,26 @@ def test_cache_that_requires_gradients_is_refused():
         c.k = torch.autograd.forward_ad.make_dual(c.k, torch.ones_like(c.k))
         with pytest.raises(ValueError, match="tangent"):
             vdm.vdm_cache_read(c, i[:1], i[None], i, out=out)
+
+
+# ----------------------------------------------------------------- caches
+
+def test_both_readers_of_a_cache_refuse_the_same():
+    """KVCache.cstruct and the native calls check a cache each for itself."""
+    g = vdm.KVCache.create(4, 16, 2, 64, dtype="e4m3", device="cpu")
+    b = vdm.KVCache.create(4, 16, 2, 64, device="cpu")
+    i = torch.zeros(2, dtype=torch.int32)
+    out = (torch.zeros(1, 2, 64, dtype=torch.bfloat16),) * 2
+    native = lambda c: vdm.vdm_cache_read(c, i[:1], i[None], i, out=out)
+    for good in (g, b, vdm.KVCache(g.k.view(torch.float8_e4m3fn), g.v.view(torch.float8_e4m3fn), g.k_scale, g.v_scale)):
+        good.cstruct()
+        with pytest.raises(ValueError, match="CUDA"):
+            native(good)
+    for bad in (vdm.KVCache(g.k, g.v), vdm.KVCache(g.k, g.v, g.k_scale, g.v_scale.int()), vdm.KVCache(g.k, g.v, g.k_scale[:3], g.v_scale),
+                vdm.KVCache(g.k, g.v, g.k_scale, g.v_scale.transpose(0, 1).contiguous().transpose(0, 1)), vdm.KVCache(g.k, g.v[:3], g.k_scale, g.v_scale),
+                vdm.KVCache(b.k, b.v.float()), vdm.KVCache(b.k.half(), b.v.half()), vdm.KVCache(b.k[0], b.v[0]),
+                vdm.KVCache(b.k[..., ::2], b.v[..., ::2]), vdm.KVCache(b.k.transpose(1, 2), b.v.transpose(1, 2))):
+        with pytest.raises(ValueError, match="cache"):
+            bad.cstruct()
+        with pytest.raises(ValueError, match="cache"):
+            native(bad)
