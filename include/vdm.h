@@ -454,7 +454,9 @@ VDM_API vdm_status vdm_surface_case_table(uint8_t* ntri, uint8_t* tri);
  *     fixed size repeat the last offset).  They are not checked: with decreasing ones
  *     it is not specified which rows are written and from which keys, but nothing
  *     outside the tensors is read or written.
- *   - Sums, norms and softmax statistics are float32.                       */
+ *   - Sums, norms and softmax statistics are float32 (a head whose sum of squares
+ *     leaves its range - elements from about 10^18 on - is normalised to zeros).
+ *   - vdm_profile_begin/end do not count these calls' kernels.                 */
 typedef struct {
     void* data;              /* element [0][0][0]                                */
     int64_t stride_token;    /* in elements; ignored with one token              */

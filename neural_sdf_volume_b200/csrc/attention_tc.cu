@@ -645,9 +645,10 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         // ------------------------------------------------------------ 8-bit tiles widened to bf16
         // A thread keeps one column of 16 codes and every ROWS-th row of a tile; the next tile's are asked for once
         // this one is announced, as the announcement's fence waits for loads too.  Pages are looked up a key tile
-        // ahead, lane i those of its keys 16 i .. 16 i + 15, and rows once for keys and values.  512 and 100 tokens
-        // over 15000 and 9000, 32/8 heads: 272 us at D = 128 (bf16 pages 217), 294 at 64; looked up right before its
-        // loads, these before the announcement: 384 and 504; codes by asynchronous copies through shared memory 318 and 438.
+        // ahead, lane i those of its keys 16 i .. 16 i + 15, and rows once for keys and values.  Two chunks of up to 512
+        // tokens over up to 15000, 32/8 heads: 313 us at D = 128 (bf16 pages 216), 300 at 64.  An earlier form with pages looked
+        // up right before its loads, these before the announcement, took 384 and 504; codes by asynchronous copies through
+        // shared memory 318 and 438.
         constexpr int CH = D / 16, ROWS = 32 * C::WIDEN / CH, U = (BN + ROWS - 1) / ROWS;
         const int ct = tid - 32 * (MMA_WARP + 1), c = ct % CH, r0 = ct / CH;
         const int items = 2 * (jmax - jb);

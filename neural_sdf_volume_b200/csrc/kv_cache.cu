@@ -147,7 +147,9 @@ __global__ void __launch_bounds__(CT, 16) cache_write_kernel(const __grid_consta
 template <typename TC, typename T>
 __global__ void __launch_bounds__(CT, 20) cache_read_kernel(const __grid_constant__ CacheIo a) {
     constexpr bool E8 = sizeof(TC) == 1;
-    constexpr int U = 8, N = 16 / (int)sizeof(T);   // pieces of 16 output bytes under way, elements of one
+    // U: pieces of 16 output bytes under way, as many as keys and values of 8 heads of 128 in bf16 have for a lane.  Tokens of fewer
+    // heads have fewer: 3 heads of 128 reach half the rate (51 us for 177 MB, 8 heads 76 for 463).
+    constexpr int U = 8, N = 16 / (int)sizeof(T);   // N: elements of a piece
     const int lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * (CT / 32) + (threadIdx.x >> 5);
     if (t >= a.T) return;

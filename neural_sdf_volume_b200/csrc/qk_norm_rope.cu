@@ -16,7 +16,10 @@ namespace vdm {
 namespace {
 
 constexpr int RT = 128;   // threads per block
-constexpr int RU = 5;     // heads of a lane in flight
+// Loads of a lane under way: five of 16 bytes fit 64 registers, and with them eight blocks on an SM.  40 heads of 128 are one full
+// round of a block's four warps (73 us for 16381 tokens); other numbers leave slots of the last round empty: 24 + 2 heads of 64 use
+// seven of ten (29 us for a third of the bytes).
+constexpr int RU = 5;
 
 template <typename T> struct Vec;
 template <> struct Vec<float> {
@@ -50,8 +53,8 @@ template <> struct Vec<__nv_bfloat16> {
 };
 
 // MODE 0: no rotation, 1: interleaved pairs, 2: halves, 3: halves of a multiple of N / 2 elements: a lane then takes N / 2
-// elements of each half, so that its pairs are its own (16381 tokens of 40 heads of 128: 71 us, by an exchange through
-// shared memory 107)
+// elements of each half, so that its pairs are its own (16381 tokens of 40 heads of 128: 74 us; by an exchange through
+// shared memory, as for other halves, 145: it spills)
 template <typename T, int D, int MODE>
 __global__ void __launch_bounds__(RT, 8) qk_norm_rope_kernel(const __grid_constant__ RopeArgs a, const int wpt) {
     constexpr int N = Vec<T>::N, LPH = D / N, HPW = 32 / LPH;
