@@ -191,3 +191,90 @@ def test_a_call_that_gives_up_leaves_nan(D, kind, new, total):
     got, lse = call()
     vdm.vdm_attention_status()
     assert torch.equal(got, want) and torch.equal(lse[:new], wl[:new])
+
+
+# ----------------------------------------------------------------- smallest calls, and types and strides at their edges
+
+@pytest.mark.parametrize("dtype, kind", S.KINDS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("pages, width", [(0, 3), (4, 0), (0, 0)])
+@pytest.mark.parametrize("new", [1, 300])
+def test_no_pages_at_all(dtype, kind, D, pages, width, new):
+    """A cache without pages, a table without columns: rows without keys; nothing read, nothing written."""
+    c = vdm.KVCache.create(pages, 16, 2, D, kind)
+    table, cu = torch.zeros(1, width, dtype=torch.int32, device="cuda"), offsets([new])
+    q, out = randn(1, new + 1, 4, D, dtype=dtype), torch.full((new + 1, 4, D), 7.0, device="cuda", dtype=S.DT[dtype])
+    got, lse = vdm.vdm_attention_paged(q, c, cu, ints([width * 16]), table, out=out, want_lse=True, causal=False)
+    vdm.vdm_attention_status()
+    if width == 0:
+        assert (got[:new] == 0).all() and torch.isneginf(lse[:new]).all()
+    else:                                            # positions without a page are zeros: weights, but no values
+        assert (got[:new] == 0).all()
+    assert (out[new:] == 7.0).all()
+    x = randn(2, new, 2, D, dtype=dtype)
+    vdm.vdm_cache_write(c, x, x, cu, ints([width * 16]), table)
+    k, v = (torch.full_like(x, 5.0) for _ in "kv")
+    vdm.vdm_cache_read(c, ints([min(new, width * 16)]), table, cu, out=(k, v))
+    n = min(new, width * 16)
+    assert (k[:n] == 0).all() and (v[:n] == 0).all() and (k[n:] == 5.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 700])
+def test_queries_without_keys(dtype, n):
+    q, k = randn(1, n, 4, 64, dtype=dtype), randn(2, 0, 2, 64, dtype=dtype)
+    got, lse = vdm.vdm_attention_packed(q, k, k, offsets([n]), ints([0, 0]), want_lse=True)
+    assert (got == 0).all() and torch.isneginf(lse).all()
+    got, lse = vdm.vdm_attention_packed(q, randn(3, 40, 2, 64, dtype=dtype), randn(4, 40, 2, 64, dtype=dtype), offsets([n]), ints([40, 40]), want_lse=True)
+    assert (got == 0).all() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "e4m3"])
+@pytest.mark.parametrize("dtype", [None, torch.float32, torch.bfloat16])
+def test_cache_read_into_tensors_of_its_own(kind, dtype):
+    """The tensors that a read allocates hold the cache's rows, keys and values, in the type asked for."""
+    if kind != "e4m3" and dtype not in (None, S.DT.get(kind)):
+        with pytest.raises(vdm.VdmError):
+            vdm.vdm_cache_read(vdm.KVCache.create(1, 16, 2, 64, kind), ints([3]), ints([[0]]), offsets([3]), total=3, dtype=dtype)
+        return
+    total = [33, 1, 70]
+    c = S.Cached(kind, 3, 64, 16, total, seed=9)
+    if kind == "e4m3":                               # the codes under their own type
+        c.cache = vdm.KVCache(c.cache.k.view(torch.float8_e4m3fn), c.cache.v.view(torch.float8_e4m3fn), c.cache.k_scale, c.cache.v_scale)
+    k, v = vdm.vdm_cache_read(c.cache, c.kv_len, c.table, offsets(total), total=sum(total), dtype=dtype)
+    want_type = dtype or (torch.bfloat16 if kind == "e4m3" else S.DT[kind])
+    for got, n in ((k, "k"), (v, "v")):
+        want = torch.from_numpy(np.concatenate([c.sequence(n, b) for b in range(len(total))])).to(want_type)
+        assert got.dtype is want_type and torch.equal(got.cpu(), want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_strides_that_do_not_count(dtype):
+    """One token, or one head: its stride may be anything."""
+    for T, H in ((1, 4), (6, 1), (1, 1)):
+        q, k, v = (randn(s, T, H, 64, dtype=dtype) for s in (1, 2, 3))
+        odd = lambda x: x.as_strided(x.shape, (x.stride(0) if T > 1 else 3, x.stride(1) if H > 1 else 5, 1))
+        want = vdm.vdm_attention_packed(q, k, v, offsets([T]))
+        assert torch.equal(vdm.vdm_attention_packed(odd(q), odd(k), odd(v), offsets([T])), want)
+        g = torch.ones(64, device="cuda")
+        assert torch.equal(vdm.vdm_qk_norm_rope(odd(q), odd(k), q_gain=g)[0], vdm.vdm_qk_norm_rope(q, k, q_gain=g)[0])
+    q, k, v = randn(1, 900, 4, 64), randn(2, 900, 1, 64), randn(3, 900, 1, 64)         # large tiles, one key head
+    one = lambda x: x.as_strided(x.shape, (64, 8, 1))
+    assert torch.equal(vdm.vdm_attention_packed(q, one(k), one(v), offsets([900])), vdm.vdm_attention_packed(q, k, v, offsets([900])))
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_positions_below_zero(inter):
+    x, rope = randn(1, 4, 3, 64, dtype="f32"), vdm.Rope.make(64, interleaved=inter)
+    pos = ints([-1, -5000, -2 ** 31, 7])
+    got, _ = vdm.vdm_qk_norm_rope(x, None, pos, rope)
+    want = OS.norm_rope(np64(x), None, 0, np64(pos), np64(rope.inv_freq), inter)
+    close(got, want, 24 * U * np.abs(np64(x)).max() * 2)
+
+
+def test_heads_on_one_side_alone():
+    x, rope, pos = randn(1, 5, 4, 64), vdm.Rope.make(64), torch.arange(5, dtype=torch.int32, device="cuda")
+    q, k = vdm.vdm_qk_norm_rope(x[:, :0], x, pos, rope)
+    assert q.shape == (5, 0, 64) and torch.equal(k, vdm.vdm_qk_norm_rope(x, None, pos, rope)[0])
+    q, k = vdm.vdm_qk_norm_rope(x, x[:, :0], pos, rope)
+    assert k.shape == (5, 0, 64) and torch.equal(q, vdm.vdm_qk_norm_rope(x, None, pos, rope)[0])
